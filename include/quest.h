@@ -386,6 +386,146 @@ QUEST_API quest_status quest_recall_diagnostics(const quest_cache* cache, const 
 QUEST_API size_t quest_diag_workspace_size(int32_t h_kv, int32_t group, int32_t nnz,
                                            int32_t page_size);
 
+/*
+ * Rotary position embedding of quest_rope_append_kv. The first rotary_dim
+ * dims of a head are rotary_dim / 2 pairs; pair j at position p turns by the
+ * angle p * inv_freq[j]:
+ *   y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin.
+ * The other dims pass through.
+ *   inv_freq    : device fp64 [rotary_dim / 2], finite, radians per position
+ *                 (base^(-2j / rotary_dim), or any scaled variant of it)
+ *   positions   : device int32 [n_new], or NULL: the token's place in its
+ *                 request's cache
+ *   rotary_dim  : a multiple of 16, 16 <= rotary_dim <= head_dim
+ *   interleaved : 0 pairs dims (j, j + rotary_dim / 2); 1 pairs (2j, 2j + 1)
+ */
+typedef struct quest_rope {
+  const double* inv_freq;
+  const int32_t* positions;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} quest_rope;
+
+/*
+ * quest_rope_append_kv — quest_append_kv with the position rotation applied
+ * on the way (Quest page §1.1: the summary has to describe the rotated keys):
+ * keys are rotated, rounded to dtype, written to their pages and folded into
+ * the page summaries exactly as quest_append_kv does with keys that are
+ * rotated already; values are copied; the queries of the same tokens are
+ * rotated into q_out. Angles are taken modulo one turn in 64-bit fixed point
+ * (about 2^-53 turns per position), so far positions keep fp32 accuracy.
+ *   q               : device dtype, token i's h_kv * group heads of head_dim at
+ *                     q + i * q_stride; NULL (with q_out NULL): K and V only
+ *   k_new, v_new    : device dtype, token i's h_kv heads at k_new + i *
+ *                     k_stride, v_new + i * v_stride
+ *   *_stride        : elements between tokens, at least the row's length and a
+ *                     multiple of 16 bytes (the parts of one fused projection
+ *                     may be passed in place)
+ *   q_out           : device dtype [n_new, h_kv * group, head_dim] (written);
+ *                     may be q itself where q_stride is the row's length
+ *   n_new, append_indptr, seq_lens_before : as quest_append_kv. Rows from
+ *                     append_indptr[batch] on are not touched.
+ * A token beyond the page table, or of a page outside the pool, is reported
+ * as in quest_append_kv: its K and V are skipped, its query is still rotated.
+ */
+QUEST_API quest_status quest_rope_append_kv(const quest_cache* cache, const quest_pages* pages,
+                                            const quest_rope* rope, const void* q,
+                                            const void* k_new, const void* v_new,
+                                            int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                            int32_t n_new, int32_t group,
+                                            const int32_t* append_indptr,
+                                            const int32_t* seq_lens_before, void* q_out,
+                                            void* stream);
+
+/*
+ * What quest_dense_decode_attn and quest_prefill_attn do to a logit before
+ * the softmax, and which keys a query sees. For the query at position p of
+ * its request (row i of q, query head h) and the key at position j:
+ *   x = sm_scale * q.k;  softcap > 0: x = softcap * tanh(x / softcap);
+ *   alibi_slopes:        x = x - alibi_slopes[h] * |p - j|
+ *   visible: lo <= j < hi,  hi = min(seq_len, max(p + 1, prefix_lens[r])),
+ *            lo = max(0, p - window + 1 if window > 0, doc_starts[i])
+ * A query that sees no key gets out = 0, lse = -inf.
+ *   alibi_slopes : device fp32 [h_kv * group], or NULL (no distance bias)
+ *   doc_starts   : device int32 [query rows], or NULL: the first position of
+ *                  the row's document (packed documents: a row sees no key of
+ *                  an earlier one)
+ *   prefix_lens  : device int32 [batch], or NULL: keys every query of the
+ *                  request sees (a prefix that attends in both directions)
+ *   softcap      : finite, 0 = none
+ *   window       : keys a query sees at most, its own included; 0 = all
+ */
+typedef struct quest_score_mods {
+  const float* alibi_slopes;
+  const int32_t* doc_starts;
+  const int32_t* prefix_lens;
+  float softcap;
+  int32_t window;
+} quest_score_mods;
+
+/*
+ * quest_dense_decode_attn — attention of one new token per request over all of
+ * its visible keys (the dense layers of Quest page §1 and §1.2), read through
+ * the page table itself: no scores, no selection lists. The query's position
+ * is seq_lens[r] - 1 (pages->seq_lens includes the new token). The (KV head,
+ * page) items of all requests are cut into equal runs, one per CTA, whatever
+ * the requests' lengths; a row cut over several CTAs is joined by log-sum-exp
+ * by the CTA that finishes last, always in the same order.
+ *   q, group, out, lse, sm_scale : as quest_sparse_decode_attn
+ *   mods      : NULL, or as above with one doc_starts entry per request
+ *   workspace : device, >= quest_dense_decode_workspace_size(...) bytes, 16-B
+ *               aligned, ZERO-FILLED before its first use; a call leaves its
+ *               counters at zero again. Calls that share a workspace must not
+ *               overlap on the GPU.
+ * A page outside the pool is skipped (QUEST_DEVERR_PAGE_RANGE), a request's
+ * tokens beyond its page table too (QUEST_DEVERR_TABLE_RANGE). Keys and values
+ * of the seq_lens[r] valid tokens must be finite, also where a query does not
+ * see them; other slots of a page may hold anything.
+ */
+QUEST_API quest_status quest_dense_decode_attn(const quest_cache* cache, const quest_pages* pages,
+                                               const void* q, int32_t group,
+                                               const quest_score_mods* mods, float* out,
+                                               float* lse, float sm_scale, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes quest_dense_decode_attn needs for these sizes on the current
+ * device (0 for unsupported shapes). */
+QUEST_API size_t quest_dense_decode_workspace_size(int32_t batch, int32_t nnz, int32_t h_kv,
+                                                   int32_t group, int32_t head_dim,
+                                                   int32_t page_size, int32_t dtype);
+
+/*
+ * quest_prefill_attn — attention of the new tokens of each request (a prompt,
+ * a chunk of one, a few drafted tokens) over its paged cache, which already
+ * holds their keys and values. Rows q_indptr[r] <= i < q_indptr[r + 1] are the
+ * request's last tokens: row i sits at position seq_lens[r] - n_r + (i -
+ * q_indptr[r]), n_r rows in all. Causal unless mods->prefix_lens opens a
+ * prefix.
+ *   q        : device dtype [n_q, h_kv * group, head_dim]
+ *   q_indptr : device int32 [batch + 1], q_indptr[0] = 0
+ *   n_q      : host, total rows (>= q_indptr[batch]; rows from there on are not
+ *              touched in out and lse)
+ *   mods     : NULL, or as above
+ *   out      : device dtype [n_q, h_kv * group, head_dim]
+ *   lse      : device fp32 [n_q, h_kv * group], or NULL
+ *   workspace: device, >= quest_prefill_workspace_size(...) bytes, 16-B
+ *              aligned, ZERO-FILLED before its first use; as in
+ *              quest_dense_decode_attn
+ * fp16: the products run on the tensor cores with fp32 accumulation, softmax
+ * weights rounded to fp16. Errors and finiteness as quest_dense_decode_attn.
+ */
+QUEST_API quest_status quest_prefill_attn(const quest_cache* cache, const quest_pages* pages,
+                                          const void* q, int32_t group, const int32_t* q_indptr,
+                                          int32_t n_q, const quest_score_mods* mods, void* out,
+                                          float* lse, float sm_scale, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Workspace bytes quest_prefill_attn needs for these sizes on the current
+ * device (0 for unsupported shapes). */
+QUEST_API size_t quest_prefill_workspace_size(int32_t batch, int32_t n_q, int32_t nnz,
+                                              int32_t h_kv, int32_t group, int32_t head_dim,
+                                              int32_t page_size, int32_t dtype);
+
 /* Phase trace of quest_decode_step (profiling aid, off by default): with a
  * device buffer of at least 16 * max_ctas uint64 set, each later call whose
  * grid has at most max_ctas CTAs writes, per CTA, 16 %globaltimer stamps (ns;

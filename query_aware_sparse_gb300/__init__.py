@@ -40,6 +40,17 @@ class QuestPages(ctypes.Structure):
                 ("nnz", ctypes.c_int32)]
 
 
+class QuestRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class QuestScoreMods(ctypes.Structure):
+    _fields_ = [("alibi_slopes", ctypes.c_void_p), ("doc_starts", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -81,6 +92,17 @@ def lib() -> ctypes.CDLL:
         L.quest_recall_diagnostics.restype = I32
         L.quest_diag_workspace_size.argtypes = [I32, I32, I32, I32]
         L.quest_diag_workspace_size.restype = SZ
+        I64 = ctypes.c_int64
+        L.quest_rope_append_kv.argtypes = [P, P, P, P, P, P, I64, I64, I64, I32, I32, P, P, P, P]
+        L.quest_rope_append_kv.restype = I32
+        L.quest_dense_decode_attn.argtypes = [P, P, P, I32, P, P, P, ctypes.c_float, P, SZ, P]
+        L.quest_dense_decode_attn.restype = I32
+        L.quest_dense_decode_workspace_size.argtypes = [I32, I32, I32, I32, I32, I32, I32]
+        L.quest_dense_decode_workspace_size.restype = SZ
+        L.quest_prefill_attn.argtypes = [P, P, P, I32, P, I32, P, P, P, ctypes.c_float, P, SZ, P]
+        L.quest_prefill_attn.restype = I32
+        L.quest_prefill_workspace_size.argtypes = [I32, I32, I32, I32, I32, I32, I32, I32]
+        L.quest_prefill_workspace_size.restype = SZ
         L.quest_set_trace.argtypes = [P, I32, I32, I32, I32, I32, I32, I32, I32]
         L.quest_set_trace.restype = I32
         L.quest_test_step_fault.argtypes = [I32, I32]
@@ -101,7 +123,10 @@ EXPORTED = ("quest_append_kv", "quest_score_pages", "quest_score_pages_per_head"
             "quest_sparse_decode_attn", "quest_sparse_decode_attn_noalloc",
             "quest_attn_workspace_size",
             "quest_decode_step", "quest_decode_workspace_size", "quest_decode_step_kernel",
-            "quest_recall_diagnostics", "quest_diag_workspace_size", "quest_set_trace",
+            "quest_recall_diagnostics", "quest_diag_workspace_size",
+            "quest_rope_append_kv", "quest_dense_decode_attn",
+            "quest_dense_decode_workspace_size", "quest_prefill_attn",
+            "quest_prefill_workspace_size", "quest_set_trace",
             "quest_test_step_fault", "quest_get_device_error", "quest_status_string")
 
 
@@ -346,6 +371,164 @@ def decode_step_kernel(batch, h_kv, group, head_dim, page_size, dtype, k, summar
                                            int(page_size), dtype_code(dtype), int(k),
                                            int(bool(summary_fp8))))
     return {2: "cstep_kernel", 1: "step_kernel"}.get(r, "")
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """Angles per position of the plain rotation, base^(-2j / rotary_dim): fp64
+    [rotary_dim / 2]. Scaled variants are any other fp64 tensor of that shape."""
+    j = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    return base ** (-j / rotary_dim)
+
+
+def _expect(name, t, dtype, shape, device, rows=False):
+    """Raises unless t is a dense tensor of this type, shape and device (with
+    ``rows``, only each row of the first dimension has to be dense)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if not (t.is_contiguous() or
+            (rows and t.shape[0] > 1 and t[0].is_contiguous() and t.stride(0) >= t[0].numel())):
+        raise ValueError(f"{name} must be contiguous" + (" within its rows" if rows else ""))
+
+
+def _current(cache: PagedCache):
+    dev = cache.k_pool.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache must be on the current CUDA device, not {dev}")
+    return dev
+
+
+def _zeros(n, dev, stream):
+    """A zeroed workspace, filled on the stream that will use it."""
+    with torch.cuda.stream(stream):
+        return torch.zeros(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_indptr,
+                   seq_lens_before, inv_freq, group: int, q_out=None, positions=None,
+                   interleaved: bool = False, stream=None):
+    """quest_rope_append_kv: rotates k_new [n_new, h_kv, d] into the pages with
+    v_new, updates the summaries, and returns q [n_new, h_kv * group, d]
+    rotated (q may be None). Tokens may be strided (the parts of one fused
+    projection); inv_freq is fp64 [rotary_dim / 2] (see rope_frequencies);
+    positions int32 [n_new] replaces the tokens' places in the cache."""
+    dev, dt, n = _current(cache), cache.dtype, k_new.shape[0]
+    h, d = cache.h_kv, cache.head_dim
+    _expect("k_new", k_new, dt, (n, h, d), dev, rows=True)
+    _expect("v_new", v_new, dt, (n, h, d), dev, rows=True)
+    _expect("append_indptr", append_indptr, torch.int32, (table.batch + 1,), dev)
+    _expect("seq_lens_before", seq_lens_before, torch.int32, (table.batch,), dev)
+    _expect("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
+    if positions is not None:
+        _expect("positions", positions, torch.int32, (n,), dev)
+    if q is not None:
+        _expect("q", q, dt, (n, h * group, d), dev, rows=True)
+        if q_out is None:
+            q_out = torch.empty((n, h * group, d), dtype=dt, device=dev)
+        _expect("q_out", q_out, dt, (n, h * group, d), dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rope = QuestRope(_ptr(inv_freq), _ptr(positions), 2 * inv_freq.numel(), int(bool(interleaved)))
+    _check(lib().quest_rope_append_kv(
+        ctypes.byref(cache.c), ctypes.byref(table.c), ctypes.byref(rope), _ptr(q), _ptr(k_new),
+        _ptr(v_new), 0 if q is None else _row_stride(q), _row_stride(k_new), _row_stride(v_new),
+        int(n), int(group), _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out),
+        _stream(stream)))
+    return q_out
+
+
+class ScoreMods:
+    """quest_score_mods: softcap, window, and device tensors alibi_slopes fp32
+    [h_q], doc_starts int32 [query rows], prefix_lens int32 [batch] (each may be
+    None), kept alive here."""
+
+    def __init__(self, softcap: float = 0.0, window: int = 0, alibi_slopes=None, doc_starts=None,
+                 prefix_lens=None):
+        self.softcap, self.window = float(softcap), int(window)
+        self.alibi_slopes, self.doc_starts, self.prefix_lens = alibi_slopes, doc_starts, prefix_lens
+        self.c = QuestScoreMods(_ptr(alibi_slopes), _ptr(doc_starts), _ptr(prefix_lens),
+                                self.softcap, self.window)
+
+    def check(self, h_q, rows, batch, device):
+        if self.alibi_slopes is not None:
+            _expect("alibi_slopes", self.alibi_slopes, torch.float32, (h_q,), device)
+        if self.doc_starts is not None:
+            _expect("doc_starts", self.doc_starts, torch.int32, (rows,), device)
+        if self.prefix_lens is not None:
+            _expect("prefix_lens", self.prefix_lens, torch.int32, (batch,), device)
+
+
+def dense_decode_workspace_size(batch, nnz, h_kv, group, head_dim, page_size, dtype) -> int:
+    return int(lib().quest_dense_decode_workspace_size(batch, nnz, h_kv, group, head_dim,
+                                                       page_size, dtype_code(dtype)))
+
+
+def dense_decode_attn(cache: PagedCache, table: PageTable, q, group: int, out=None, lse=None,
+                      sm_scale: float = 0.0, mods: ScoreMods | None = None, workspace=None,
+                      stream=None):
+    """quest_dense_decode_attn: (out [B, h_q, d] fp32, lse [B, h_q] fp32) of one
+    query per request over all of its cached tokens. ``workspace``: uint8,
+    dense_decode_workspace_size bytes, zero-filled before its first use."""
+    dev, h_q, d = _current(cache), cache.h_kv * group, cache.head_dim
+    B = table.batch
+    _expect("q", q, cache.dtype, (B, h_q, d), dev)
+    if out is None:
+        out = torch.empty((B, h_q, d), dtype=torch.float32, device=dev)
+    if lse is None:
+        lse = torch.empty((B, h_q), dtype=torch.float32, device=dev)
+    _expect("out", out, torch.float32, (B, h_q, d), dev)
+    _expect("lse", lse, torch.float32, (B, h_q), dev)
+    if mods is not None:
+        mods.check(h_q, B, B, dev)
+    if workspace is None:
+        n = dense_decode_workspace_size(B, table.nnz, cache.h_kv, group, d, cache.page_size,
+                                        cache.dtype)
+        workspace = _zeros(n, dev, stream)
+    _check(lib().quest_dense_decode_attn(
+        ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q), int(group),
+        None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
+        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _stream(stream)))
+    return out, lse
+
+
+def prefill_workspace_size(batch, n_q, nnz, h_kv, group, head_dim, page_size, dtype) -> int:
+    return int(lib().quest_prefill_workspace_size(batch, n_q, nnz, h_kv, group, head_dim,
+                                                  page_size, dtype_code(dtype)))
+
+
+def prefill_attn(cache: PagedCache, table: PageTable, q, group: int, q_indptr, out=None, lse=None,
+                 sm_scale: float = 0.0, mods: ScoreMods | None = None, workspace=None,
+                 stream=None):
+    """quest_prefill_attn: (out [n_q, h_q, d] in the cache's type, lse [n_q, h_q]
+    fp32) of each request's last tokens, rows q_indptr[r] .. q_indptr[r + 1] of
+    q, over its cached tokens. ``workspace``: uint8, prefill_workspace_size
+    bytes, zero-filled before its first use."""
+    dev, h_q, d = _current(cache), cache.h_kv * group, cache.head_dim
+    n = q.shape[0]
+    _expect("q", q, cache.dtype, (n, h_q, d), dev)
+    _expect("q_indptr", q_indptr, torch.int32, (table.batch + 1,), dev)
+    if out is None:
+        out = torch.empty((n, h_q, d), dtype=cache.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((n, h_q), dtype=torch.float32, device=dev)
+    _expect("out", out, cache.dtype, (n, h_q, d), dev)
+    _expect("lse", lse, torch.float32, (n, h_q), dev)
+    if mods is not None:
+        mods.check(h_q, n, table.batch, dev)
+    if workspace is None:
+        size = prefill_workspace_size(table.batch, n, table.nnz, cache.h_kv, group, d,
+                                      cache.page_size, cache.dtype)
+        workspace = _zeros(size, dev, stream)
+    _check(lib().quest_prefill_attn(
+        ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q), int(group), _ptr(q_indptr), int(n),
+        None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
+        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _stream(stream)))
+    return out, lse
 
 
 TRACE_NAMES = ("start", "scored", "selected", "att_start", "att_pages", "att_merged",

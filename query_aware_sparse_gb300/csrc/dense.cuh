@@ -1,0 +1,31 @@
+// Device helpers shared by the dense-layer operators: which keys a query row
+// sees and what happens to a logit before the softmax.
+#pragma once
+
+#include "common.cuh"
+#include "dense.h"
+
+namespace quest {
+
+// Visible keys lo <= j < hi of the row at position pos of a request of len
+// tokens (hi <= lo: none). doc and prefix are 0 where the call has none.
+struct Seen { int lo, hi; };
+__device__ __forceinline__ Seen seen_keys(int pos, int len, int window, int doc, int prefix) {
+  Seen s;
+  s.hi = min(len, max(pos + 1, prefix));
+  s.lo = max(0, doc);
+  if (window > 0 && pos >= window) s.lo = max(s.lo, pos - window + 1);
+  return s;
+}
+
+// A request's tokens that its page table holds.
+__device__ __forceinline__ int held_tokens(int len, int table_pages, int page_size, unsigned* err) {
+  if (len <= 0) return 0;
+  if ((len - 1) / page_size >= table_pages) {
+    report(err, QUEST_DEVERR_TABLE_RANGE);
+    return max(0, table_pages) * page_size;
+  }
+  return len;
+}
+
+}  // namespace quest

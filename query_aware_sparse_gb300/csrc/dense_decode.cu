@@ -1,0 +1,22 @@
+// Dense decode attention: one query row per request over its paged cache.
+#include "dense_rows.cuh"
+
+namespace quest {
+
+size_t dense_decode_workspace(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) {
+  return 16;
+}
+
+cudaError_t launch_dense_decode(const DenseArgs& a, cudaStream_t s) {
+  const dim3 grid(a.batch, a.h_kv * a.group);
+  if (a.dtype == QUEST_F16) {
+    if (a.head_dim == 128) dense_rows_kernel<__half, float, 128><<<grid, kRowThreads, 0, s>>>(a);
+    else dense_rows_kernel<__half, float, 64><<<grid, kRowThreads, 0, s>>>(a);
+  } else {
+    if (a.head_dim == 128) dense_rows_kernel<float, float, 128><<<grid, kRowThreads, 0, s>>>(a);
+    else dense_rows_kernel<float, float, 64><<<grid, kRowThreads, 0, s>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace quest
