@@ -23,11 +23,21 @@ SOURCES = ["quest_api.cu", "append.cu", "score.cu", "select.cu", "attn.cu", "ste
            "step_e4m3_d64.cu", "step_e4m3_d128.cu", "noalloc.cu", "diag.cu", "union.cu",
            "cstep_f32_d64.cu", "cstep_f32_d128.cu", "cstep_f16_d64.cu", "cstep_f16_d128.cu",
            "cstep_e4m3_d64.cu", "cstep_e4m3_d128.cu",
-           "dense_api.cu", "rope_append.cu", "dense_decode.cu", "prefill.cu"]
-HEADERS = [os.path.join(CSRC, h) for h in ("common.cuh", "internal.h", "topk.cuh", "attn_dev.cuh",
-                                           "attn_mma.cuh", "step_impl.cuh",
-                                           "cstep_impl.cuh", "dense.h", "dense.cuh", "dense_rows.cuh")] + [
-           os.path.join(ROOT, "include", "quest.h")]
+           "dense_api.cu", "rope_append.cu", "dense_decode.cu", "prefill.cu",
+           "prefill_f16_d64_t1.cu", "prefill_f16_d64_t2.cu", "prefill_f16_d128_t1.cu",
+           "prefill_f16_d128_t2.cu"]
+SHARED_HEADERS = ("common.cuh", "internal.h")
+STEP_HEADERS = ("topk.cuh", "attn_dev.cuh", "attn_mma.cuh", "step_impl.cuh", "cstep_impl.cuh")
+DENSE_HEADERS = ("dense.h", "dense.cuh", "dense_rows.cuh", "tc.cuh", "prefill_mma.cuh")
+
+
+def headers_of(src):
+    """Headers whose change rebuilds a source file."""
+    own = DENSE_HEADERS if src.startswith(("dense", "prefill", "rope")) else STEP_HEADERS
+    return [os.path.join(CSRC, h) for h in SHARED_HEADERS + own] + [
+        os.path.join(ROOT, "include", "quest.h")]
+
+
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -49,14 +59,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile and link libquest.so; returns its path."""
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
-    hdr_time = max(_mtime(h) for h in HEADERS)
     jobs = []
     objs = []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
         o = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
         objs.append(o)
-        if force or _mtime(o) < max(_mtime(s), hdr_time):
+        if force or _mtime(o) < max(_mtime(h) for h in [s] + headers_of(src)):
             jobs.append([nvcc, *FLAGS, *extra_flags, "-c", s, "-o", o])
 
     def run(cmd):

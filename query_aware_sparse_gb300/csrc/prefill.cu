@@ -1,21 +1,125 @@
-// Prompt attention: the new tokens of each request over its paged cache.
+// Prompt attention: the new tokens of each request over its paged cache. Plan,
+// tensor maps and dispatch; fp16 on the tensor cores (prefill_mma.cuh).
 #include "dense_rows.cuh"
+#include "internal.h"
+#include "prefill_mma.cuh"
 
 namespace quest {
 
-size_t prefill_workspace(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) {
-  return 16;
+#define QUEST_PREFILL_VARIANT(d, t) \
+  cudaError_t launch_prefill_f16_d##d##_t##t(const PrefillMaps& maps, const PrefillArgs& p, cudaStream_t s);
+QUEST_PREFILL_VARIANT(64, 1)
+QUEST_PREFILL_VARIANT(64, 2)
+QUEST_PREFILL_VARIANT(128, 1)
+QUEST_PREFILL_VARIANT(128, 2)
+#undef QUEST_PREFILL_VARIANT
+
+namespace {
+
+struct Plan {
+  int tiles, blocks, splits;
+  size_t lse_at, bytes;               // of the partial results in the workspace
+};
+
+int sm_count() {
+  int dev = 0, sms = 152;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();
+  return sms;
+}
+
+Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
+                  int32_t head_dim, int32_t page_size, int32_t dtype) {
+  Plan p{1, 0, 1, 0, 16};
+  if (dtype != QUEST_F16 || n_q == 0 || batch == 0) return p;
+  // two tiles where the requests' rows fill more than one on average
+  p.tiles = (long long)n_q * group > 128LL * batch ? 2 : 1;
+  const int tokens = p.tiles * 128 / group;
+  const long long blocks = (long long)n_q / tokens + batch;
+  p.blocks = (int)(blocks < n_q ? blocks : n_q);
+  // too few CTAs for the device: cut each one's keys
+  const long long units = (long long)p.blocks * h_kv, want = (long long)sm_count() * (p.tiles == 2 ? 1 : 4);
+  const int bn = p.tiles == 2 ? 128 : 64;
+  const long long key_blocks = ((long long)nnz * page_size / batch + bn - 1) / bn;
+  if (units < want) {
+    long long s = (want + units - 1) / units;
+    if (s > (key_blocks + 1) / 2) s = (key_blocks + 1) / 2;
+    if (s > 1) p.splits = (int)s;
+  }
+  if (p.splits > 1) {
+    const size_t rows = (size_t)p.splits * n_q * h_kv * group;
+    p.lse_at = rows * head_dim * sizeof(float);
+    p.bytes = p.lse_at + rows * sizeof(float);
+  }
+  return p;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled f = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<EncodeTiled>(fn);
+  }();
+  return f;
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[3] = {1, 1, 1};
+  const EncodeTiled f = encoder();
+  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base), dims, strides,
+                box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_f16(const DenseArgs& a, cudaStream_t s) {
+  const Plan plan = plan_prefill(a.batch, a.n_q, a.nnz, a.h_kv, a.group, a.head_dim, a.page_size, a.dtype);
+  PrefillArgs p{};
+  p.a = a;
+  p.blocks = plan.blocks;
+  p.splits = plan.splits;
+  p.part_o = static_cast<float*>(a.workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.lse_at);
+  p.wait_limit = wait_limit();
+  PrefillMaps maps;
+  const cuuint64_t d = a.head_dim, hq = (cuuint64_t)a.h_kv * a.group;
+  // queries: a box is one tile's tokens with their group's heads, 64 dims
+  const cuuint64_t q_dims[3] = {d, hq, (cuuint64_t)a.n_q}, q_strides[2] = {d * 2, hq * d * 2};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(128 / a.group)};
+  // pools: a box is one page of one KV head, 64 dims
+  const cuuint64_t p_dims[2] = {d, (cuuint64_t)a.n_phys * a.h_kv * a.page_size}, p_strides[1] = {d * 2};
+  const cuuint32_t p_box[2] = {64, (cuuint32_t)a.page_size};
+  if (!encode(&maps.q, a.q, 3, q_dims, q_strides, q_box) ||
+      !encode(&maps.k, a.k_pool, 2, p_dims, p_strides, p_box) ||
+      !encode(&maps.v, a.v_pool, 2, p_dims, p_strides, p_box))
+    return cudaErrorInvalidValue;
+  if (a.head_dim == 128)
+    return plan.tiles == 2 ? launch_prefill_f16_d128_t2(maps, p, s) : launch_prefill_f16_d128_t1(maps, p, s);
+  return plan.tiles == 2 ? launch_prefill_f16_d64_t2(maps, p, s) : launch_prefill_f16_d64_t1(maps, p, s);
+}
+
+}  // namespace
+
+size_t prefill_workspace(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
+                         int32_t head_dim, int32_t page_size, int32_t dtype) {
+  return plan_prefill(batch, n_q, nnz, h_kv, group, head_dim, page_size, dtype).bytes;
 }
 
 cudaError_t launch_prefill(const DenseArgs& a, cudaStream_t s) {
+  if (a.dtype == QUEST_F16) return launch_f16(a, s);
   const dim3 grid(a.n_q, a.h_kv * a.group);
-  if (a.dtype == QUEST_F16) {
-    if (a.head_dim == 128) dense_rows_kernel<__half, __half, 128><<<grid, kRowThreads, 0, s>>>(a);
-    else dense_rows_kernel<__half, __half, 64><<<grid, kRowThreads, 0, s>>>(a);
-  } else {
-    if (a.head_dim == 128) dense_rows_kernel<float, float, 128><<<grid, kRowThreads, 0, s>>>(a);
-    else dense_rows_kernel<float, float, 64><<<grid, kRowThreads, 0, s>>>(a);
-  }
+  if (a.head_dim == 128) dense_rows_kernel<float, float, 128><<<grid, kRowThreads, 0, s>>>(a);
+  else dense_rows_kernel<float, float, 64><<<grid, kRowThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -1,0 +1,548 @@
+// Prompt attention on the tensor cores, fp16 (quest_prefill_attn).
+//
+// Mathematics. For a block of query rows (the tokens of one request times the
+// group's heads, head fastest) and one KV head: over blocks of BN keys
+//   S = Q K^T;  x = mods(S) in base 2, -inf where a row does not see the key;
+//   m' = max(m, max x);  P = 2^(x - m' + 6);  l += sum P;  O += P V
+// and O / l at the end. The running maximum is let lag behind by up to 2^8
+// before O is rescaled, so rescaling is rare; the factor 2^6 keeps small
+// weights out of fp16's subnormal range (P < 2^14). P is rounded to fp16 (half
+// a step, 2^-11 of itself) because the second product takes fp16 operands;
+// S, O, m and l stay in fp32.
+//
+// Bound. 4 D flops per (row, visible key) on tcgen05 against 2 D bytes per key
+// and KV head: tensor bound from a few hundred rows on. The softmax runs one
+// exponential per (row, key) next to it.
+//
+// Shape. TILES row tiles of 128 (one accumulator lane per row). With two tiles
+// (256 rows, BN = 128) one tile's softmax runs while the tensor core works on
+// the other. With one (few rows; BN = 64) the next block's S is issued before
+// the softmax of the last, and two CTAs share an SM. Warps 0-3 (and 4-7) are
+// the softmax of a tile, one row per thread; then one warp loads, one issues.
+//   shared memory: Q [TILES][D/64][128 rows][64], then a ring of K and V blocks
+//     [D/64][BN keys][64] in order K V K V, all rows of 128 bytes with the
+//     128-byte swizzle, K and V copied by one TMA box per page and 64 dims;
+//   TMEM: S (P takes its place, two fp16 per column) and O, fp32.
+// K and V of a block are used by both tiles before their place is refilled.
+// Rows of V that hold no valid token are zeroed in shared memory (0 * NaN of a
+// stale slot would be NaN); such keys' S is replaced, never added to.
+#pragma once
+
+#include "dense.cuh"
+#include "tc.cuh"
+
+namespace quest {
+
+struct PrefillMaps { CUtensorMap q, k, v; };
+
+struct PrefillArgs {
+  DenseArgs a;
+  int32_t blocks;          // row blocks, an upper bound (sum over requests)
+  int32_t splits;          // equal parts of each block's keys
+  float* part_o;           // [splits, n_q, h_q, D], normalised
+  float* part_lse;         // [splits, n_q, h_q], base 2
+  uint32_t wait_limit;
+};
+
+template <int D, int TILES> struct PrefillShape {
+  static constexpr int BN = TILES == 2 ? 128 : 64;
+  static constexpr int SBUF = TILES == 2 ? 1 : 2;              // S buffers per tile
+  static constexpr int HALVES = D / 64;
+  static constexpr uint32_t Q_TILE = 128 * D * 2, BLOCK = BN * D * 2;
+  static constexpr int STAGES = TILES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 4 : 8);
+  static constexpr uint32_t SMEM = 1024 + TILES * Q_TILE + STAGES * BLOCK;
+  static constexpr int THREADS = TILES * 128 + 64;
+  static constexpr int BOUND = TILES * 128 + 128;      // registers come in fours of warps
+  static constexpr uint32_t O_COL = TILES * SBUF * BN;         // S buffers first
+  static constexpr uint32_t TMEM = O_COL + TILES * D <= 128 ? 128 : O_COL + TILES * D <= 256 ? 256 : 512;
+  static constexpr int PER_SM = TILES == 2 ? 1 : 2;
+};
+
+// Finds row block `idx`, counted over the requests, blocks of `tokens` tokens.
+__device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int idx, int lane,
+                                           int* r_out, int* b_out) {
+  int base = 0;
+  for (int r0 = 0; r0 < a.batch; r0 += 32) {
+    const int r = r0 + lane;
+    const int n = r < a.batch ? a.q_indptr[r + 1] - a.q_indptr[r] : 0;
+    const int cnt = n > 0 ? (n + tokens - 1) / tokens : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(FULL, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int at = idx - base - (incl - cnt);
+    const unsigned hit = __ballot_sync(FULL, at >= 0 && at < cnt);
+    if (hit) {
+      *r_out = r0 + __ffs(hit) - 1;
+      *b_out = __shfl_sync(FULL, at, __ffs(hit) - 1);
+      return true;
+    }
+    base += __shfl_sync(FULL, incl, 31);
+  }
+  return false;
+}
+
+template <int D, int TILES, bool CAP, bool ALIBI>
+__global__ void __launch_bounds__(PrefillShape<D, TILES>::BOUND, PrefillShape<D, TILES>::PER_SM)
+prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p) {
+  using P = PrefillShape<D, TILES>;
+  constexpr int BN = P::BN, SBUF = P::SBUF, HALVES = P::HALVES, STAGES = P::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t q_full, full[STAGES], empty[STAGES], aux, drain;
+  __shared__ __align__(8) uint64_t s_full[TILES][SBUF], p_full[TILES][SBUF], pv_done[TILES];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_req, s_blk, s_lo[TILES], s_hi[TILES], s_bad;
+  __shared__ volatile int s_quit;
+
+  const DenseArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.group, S = a.page_size, hq = a.h_kv * G;
+  const int page_shift = S == 16 ? 4 : 5;
+  const int tile_tokens = 128 / G, block_tokens = TILES * tile_tokens;
+
+  // CTAs in order: KV head, split, then row blocks from the last on (the rows
+  // that see most keys first)
+  int b = blockIdx.x;
+  const int g = b % a.h_kv;
+  b /= a.h_kv;
+  const int split = b % p.splits;
+  const int idx = p.blocks - 1 - b / p.splits;
+
+  if (warp == 0) {
+    int r = -1, blk = 0;
+    const bool found = find_block(a, block_tokens, idx, lane, &r, &blk);
+    if (lane == 0) {
+      s_req = found ? r : -1;
+      s_blk = blk;
+      s_quit = 0;
+      s_bad = 0;
+      for (int t = 0; t < TILES; ++t) { s_lo[t] = 0x7fffffff; s_hi[t] = 0; }
+    }
+  } else if (warp == 1 && lane == 0) {
+    mbar_init(&q_full, 1);
+    mbar_init(&aux, 1);
+    mbar_init(&drain, 1);
+    for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int t = 0; t < TILES; ++t) {
+      for (int i = 0; i < SBUF; ++i) { mbar_init(&s_full[t][i], 1); mbar_init(&p_full[t][i], 128); }
+      mbar_init(&pv_done[t], 1);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const int r = s_req;
+  if (r < 0) return;                                   // past the last row block
+
+  const int row0 = a.q_indptr[r], n_r = a.q_indptr[r + 1] - row0;
+  const int e0 = a.page_indptr[r], len = a.seq_lens[r];
+  const int held = held_tokens(len, a.page_indptr[r + 1] - e0, S, threadIdx.x ? nullptr : a.err);
+  const int tok0 = s_blk * block_tokens;               // first token of the row block
+
+  // what this thread's row sees (softmax warps)
+  const int tile = warp >> 2;                          // of a softmax warp
+  const int tok = tok0 + (TILES == 2 ? tile : 0) * tile_tokens + (threadIdx.x & 127) / G;
+  const int pos = len - n_r + tok;
+  const bool softmax_warp = warp < 4 * TILES;
+  const bool valid = softmax_warp && tok < n_r;
+  Seen seen{0, 0};
+  if (valid) {
+    seen = seen_keys(pos, held, a.window, a.doc_starts ? a.doc_starts[row0 + tok] : 0,
+                     a.prefix_lens ? a.prefix_lens[r] : 0);
+    if (seen.hi <= seen.lo) seen = Seen{0, 0};
+  }
+  if (softmax_warp) {
+    const int lo = __reduce_min_sync(FULL, seen.hi > 0 ? seen.lo : 0x7fffffff);
+    const int hi = __reduce_max_sync(FULL, seen.hi);
+    if (lane == 0 && hi > 0) {
+      atomicMin(&s_lo[tile], lo);
+      atomicMax(&s_hi[tile], hi);
+    }
+  } else if (warp == 4 * TILES + 1) {
+    tmem_alloc(smem_u32(&s_tmem), P::TMEM);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  // key blocks: of the row block, of this split, of each tile
+  int u0 = s_lo[0], u1 = s_hi[0];
+  if (TILES == 2) { u0 = min(u0, s_lo[TILES - 1]); u1 = max(u1, s_hi[TILES - 1]); }
+  int n0 = u1 > 0 ? u0 / BN : 0, n1 = (u1 + BN - 1) / BN;
+  if (p.splits > 1) {
+    const int nb = n1 - n0, first = n0;
+    n0 = first + (int)((long long)nb * split / p.splits);
+    n1 = first + (int)((long long)nb * (split + 1) / p.splits);
+  }
+  int t0[TILES], t1[TILES];
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    t0[t] = s_hi[t] > 0 ? max(n0, s_lo[t] / BN) : n1;
+    t1[t] = s_hi[t] > 0 ? min(n1, (s_hi[t] + BN - 1) / BN) : n1;
+  }
+  // pages outside the pool: reported, and looked for block by block if any
+  for (int pg = n0 * BN / S + threadIdx.x; pg < min(n1 * BN, held + S - 1) / S; pg += P::THREADS) {
+    const int id = a.page_indices[e0 + pg];
+    if (id < 0 || id >= a.n_phys) s_bad = 1;
+  }
+  __syncthreads();
+  const bool any_bad = s_bad != 0;
+  if (any_bad && threadIdx.x == 0) report(a.err, QUEST_DEVERR_PAGE_RANGE);
+
+  const uint32_t q_s = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t ring = q_s + TILES * P::Q_TILE;
+  const int pages_per_block = BN / S;
+
+  if (warp == 4 * TILES) {
+    // ---- loads ----------------------------------------------------------------
+    if (n1 > n0 && lane == 0) {
+      mbar_expect_tx(&q_full, TILES * P::Q_TILE);
+#pragma unroll
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+          tma_3d(q_s + t * P::Q_TILE + h * 128 * 128, &maps.q, h * 64, g * G,
+                 row0 + tok0 + t * tile_tokens, smem_u32(&q_full));
+    }
+    const int held_pages = (held + S - 1) / S;
+    int stage = 0, done = 0;                          // stages filled so far
+    uint32_t phase = 0, aux_phase = 0;
+    bool go = true;
+    auto page_of = [&](int n) {
+      const int lp = n * pages_per_block + lane;
+      int id = -1;
+      if (lane < pages_per_block && n < n1 && lp < held_pages) id = a.page_indices[e0 + lp];
+      return id >= 0 && id < a.n_phys ? id : -1;
+    };
+    int id = page_of(n0);
+    for (int n = n0; go && n < n1; ++n) {
+      const int next = page_of(n + 1);
+      const unsigned have = __ballot_sync(FULL, id >= 0);
+      const uint32_t bytes = __popc(have) * S * D * 2;
+      const bool ragged = held < (n + 1) * BN || __popc(have) < pages_per_block;
+      const int y = id >= 0 ? (id * a.h_kv + g) * S : 0;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (done >= STAGES && !warp_wait_or_quit(&empty[stage], phase ^ 1, p.wait_limit, &s_quit)) {
+          go = false;
+          break;
+        }
+        const uint32_t dst = ring + stage * P::BLOCK;
+        uint64_t* bar = kv && ragged ? &aux : &full[stage];
+        if (lane == 0 && bytes) mbar_expect_tx(bar, bytes);
+        __syncwarp();
+        if (id >= 0) {
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_2d(dst + h * BN * 128 + lane * S * 128, kv ? &maps.v : &maps.k, h * 64, y,
+                   smem_u32(bar));
+        }
+        __syncwarp();
+        if (kv && ragged) {
+          // zero what is no valid token, then hand the block over
+          if (bytes) {
+            if (!warp_wait_or_quit(&aux, aux_phase, p.wait_limit, &s_quit)) { go = false; break; }
+            aux_phase ^= 1;
+          }
+          for (int i = lane; i < BN * HALVES * 8; i += 32) {
+            const int row = i >> 3 & (BN - 1), h = i / (8 * BN);
+            if (n * BN + row >= held || !(have >> (row >> page_shift) & 1)) {
+              const uint32_t at = dst + h * BN * 128 + row * 128 + (i & 7) * 16;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" :: "r"(at), "r"(0) : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[stage]);
+        } else if (!bytes && lane == 0) {
+          mbar_arrive(&full[stage]);
+        }
+        ++done;
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      }
+      id = next;
+    }
+    if (s_quit) {                                     // wait (bounded) for the copies in flight
+      for (int i = 0; i < STAGES && i < done; ++i)
+        for (uint32_t k = 0; k < p.wait_limit && !mbar_try_wait_sleep(&full[i], (done - 1 - i) / STAGES & 1, 1000u); ++k) {}
+      for (uint32_t k = 0; k < p.wait_limit && n1 > n0 && !mbar_try_wait_sleep(&q_full, 0, 1000u); ++k) {}
+    }
+  } else if (warp == 4 * TILES + 1) {
+    // ---- tensor core -------------------------------------------------------------
+    if (lane == 0 && n1 > n0) {
+      constexpr uint32_t ID_S = mma_idesc(128, BN, false), ID_O = mma_idesc(128, D, true);
+      // stage of K of block n is 2 (n - n0) of the ring's sequence, V the next
+      auto stage_of = [&](int seq) { return seq % STAGES; };
+      auto issue_s = [&](int t, int n) {
+        const int seq = 2 * (n - n0);
+        const uint32_t k_s = ring + stage_of(seq) * P::BLOCK, a_s = q_s + t * P::Q_TILE;
+        const int buf = SBUF == 2 ? (n - n0) & 1 : 0;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t in = (k & 3) * 32;
+          mma_ss(tmem + (t * SBUF + buf) * BN, smem_desc(a_s + (k >> 2) * 128 * 128 + in, 16, 1024),
+                 smem_desc(k_s + (k >> 2) * BN * 128 + in, 16, 1024), ID_S, k > 0);
+        }
+        mma_commit(smem_u32(&s_full[t][buf]));
+      };
+      auto wait_full = [&](int seq) {
+        return wait_or_quit(&full[stage_of(seq)], (seq / STAGES) & 1, p.wait_limit, &s_quit);
+      };
+      auto active = [&](int t, int n) {
+        return t == 0 ? n >= t0[0] && n < t1[0] : n >= t0[TILES - 1] && n < t1[TILES - 1];
+      };
+      bool go = wait_or_quit(&q_full, 0, p.wait_limit, &s_quit) && wait_full(0);
+      uint32_t p_phase = 0;                           // a bit per S buffer
+      if (go) {
+        tc_fence_after();
+        for (int t = 0; t < TILES; ++t)
+          if (active(t, n0)) issue_s(t, n0);
+        mma_commit(smem_u32(&empty[0]));
+      }
+      for (int n = n0; go && n < n1; ++n) {
+        const int seq = 2 * (n - n0);
+        const int buf = SBUF == 2 ? (n - n0) & 1 : 0;
+        if (SBUF == 2 && n + 1 < n1) {                // the next S while this softmax runs
+          if (!(go = wait_full(seq + 2))) break;
+          tc_fence_after();
+          for (int t = 0; t < TILES; ++t)
+            if (active(t, n + 1)) issue_s(t, n + 1);
+          mma_commit(smem_u32(&empty[stage_of(seq + 2)]));
+        }
+        if (!(go = wait_full(seq + 1))) break;
+        for (int t = 0; go && t < TILES; ++t) {
+          if (active(t, n)) {
+            const int bit = t * SBUF + buf;
+            if (!(go = wait_or_quit(&p_full[t][buf], p_phase >> bit & 1, p.wait_limit, &s_quit))) break;
+            p_phase ^= 1u << bit;
+            tc_fence_after();
+            const uint32_t v_s = ring + stage_of(seq + 1) * P::BLOCK;
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              mma_ts(tmem + P::O_COL + t * D, tmem + (t * SBUF + buf) * BN + k * 8,
+                     smem_desc(v_s + k * 2048, BN * 128, 1024), ID_O, n > (t == 0 ? t0[0] : t0[TILES - 1]) || k > 0);
+            mma_commit(smem_u32(&pv_done[t]));
+          }
+          if (t == TILES - 1) mma_commit(smem_u32(&empty[stage_of(seq + 1)]));
+          if (SBUF == 1 && n + 1 < n1) {
+            if (t == 0) {
+              if (!(go = wait_full(seq + 2))) break;
+              tc_fence_after();
+            }
+            if (active(t, n + 1)) issue_s(t, n + 1);
+            if (t == TILES - 1) mma_commit(smem_u32(&empty[stage_of(seq + 2)]));
+          }
+        }
+      }
+      // everything issued is done before the CTA may leave (bounded)
+      mma_commit(smem_u32(&drain));
+      for (uint32_t k = 0; k < p.wait_limit && !mbar_try_wait_sleep(&drain, 0, 1000u); ++k) {}
+    }
+  } else {
+    // ---- softmax: one row per thread ------------------------------------------------
+    const int row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
+    const int h = g * G + row % G;
+    const float log2s = a.scale * LOG2E;
+    const float cap2 = a.softcap * LOG2E, to_z = CAP ? 2.f * LOG2E * a.scale / a.softcap : 0.f;
+    const float slope2 = ALIBI && valid ? a.slopes[h] * LOG2E : 0.f;
+    const float sl2 = CAP || ALIBI ? 1.f : log2s;     // of the value the maximum is taken of
+    float m = -INFINITY, l = 0.f;
+    uint32_t s_phase = 0;                             // a bit per S buffer
+    bool ok = true;
+    const int first = tile == 0 ? t0[0] : t0[TILES - 1], last = tile == 0 ? t1[0] : t1[TILES - 1];
+    const uint32_t o_col = tmem + lanes + P::O_COL + tile * D;
+    for (int n = first; n < last; ++n) {
+      const int buf = SBUF == 2 ? (n - n0) & 1 : 0;
+      const uint32_t s_col = tmem + lanes + (tile * SBUF + buf) * BN;
+      unsigned bad = 0;
+      if (any_bad) {
+        const int lp = n * pages_per_block + lane;
+        const int id = lane < pages_per_block && lp * S < held ? a.page_indices[e0 + lp] : 0;
+        bad = __ballot_sync(FULL, id < 0 || id >= a.n_phys);
+      }
+      if (!(ok = warp_wait_or_quit(&s_full[tile][buf], s_phase >> buf & 1, p.wait_limit, &s_quit))) break;
+      s_phase ^= 1u << buf;
+      tc_fence_after();
+      uint32_t sv[BN / 32][32];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + c * 32, sv[c]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) tmem_loaded(sv[c]);
+      float x[BN];
+#pragma unroll
+      for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
+      const int kb = n * BN;
+      if (CAP) {
+        // cap tanh(z / 2) = cap (1 - 2 / (1 + e^z)), in base 2
+#pragma unroll
+        for (int c = 0; c < BN; ++c) x[c] = fmaf(rcp(1.f + ex2(x[c] * to_z)), -2.f * cap2, cap2);
+      }
+      if (ALIBI) {
+        const float d0 = (float)(pos - kb);
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          x[c] = fmaf(fabsf(d0 - (float)c), -slope2, CAP ? x[c] : x[c] * log2s);
+      }
+      if (__any_sync(FULL, kb < seen.lo || kb + BN > seen.hi || bad)) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c)
+          if (kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1)) x[c] = -INFINITY;
+      }
+      float mx = x[0];
+#pragma unroll
+      for (int c = 1; c < BN; ++c) mx = fmaxf(mx, x[c]);
+      mx *= sl2;
+      const bool grow = mx > m + 8.f;                 // also the first finite maximum
+      if (__any_sync(FULL, grow)) {
+        const float f = grow ? ex2(m - mx) : 1.f;     // m = -inf: O and l are zero, f = 0
+        if (n > first) {
+          if (!(ok = warp_wait_or_quit(&pv_done[tile], (n - 1 - first) & 1, p.wait_limit, &s_quit)))
+            break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_col + c * 32, o);
+            tmem_wait_ld();
+            tmem_loaded(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(o_col + c * 32, o);
+          }
+        }
+        l *= f;
+        if (grow) m = mx;
+      }
+      const float mu = m == -INFINITY ? 0.f : m - 6.f;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < BN / 64; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float pa = ex2(fmaf(x[c * 64 + 2 * e], sl2, -mu));
+          const float pb = ex2(fmaf(x[c * 64 + 2 * e + 1], sl2, -mu));
+          sum0 += pa;
+          sum1 += pb;
+          const __half2 hh = __floats2half2_rn(pa, pb);
+          w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+        }
+        tmem_st32(s_col + c * 32, w);
+      }
+      l += sum0 + sum1;
+      tmem_wait_st();
+      // the last block's product: done by now, and a wait on the next phase
+      // would pass at once while this one is open
+      if (n > first &&
+          !(ok = warp_wait_or_quit(&pv_done[tile], (n - 1 - first) & 1, p.wait_limit, &s_quit)))
+        break;
+      tc_fence_before();
+      mbar_arrive(&p_full[tile][buf]);
+    }
+    // ---- O / l ------------------------------------------------------------------------
+    if (ok && last > first)
+      ok = warp_wait_or_quit(&pv_done[tile], (last - 1 - first) & 1, p.wait_limit, &s_quit);
+    if (ok) {
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? m - 6.f + lg2(l) : -INFINITY;
+      const size_t at = ((size_t)row0 + tok) * hq + h;
+      const size_t part = (size_t)split * a.n_q * hq + at;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (last > first) {
+          tmem_ld32(o_col + c * 32, o);
+          tmem_wait_ld();
+          tmem_loaded(o);
+        }
+        if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = last > first ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          if (p.splits > 1) {
+            float* dst = p.part_o + part * D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) st_v4(dst + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+          } else {
+            __half* dst = static_cast<__half*>(a.out) + at * D + c * 32;
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const __half2 hh = __floats2half2_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+              w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) st_v4(dst + 2 * e, make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]));
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        if (p.splits > 1) p.part_lse[part] = lse2;
+        else if (a.lse) a.lse[at] = lse2 * LN2;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (s_quit && threadIdx.x == 0) report(a.err, QUEST_DEVERR_WAIT_TIMEOUT);
+  if (warp == 4 * TILES + 1) tmem_free(tmem, P::TMEM);
+}
+
+// Joins the splits of each row by log-sum-exp: one warp per (row, query head).
+template <int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) {
+  const DenseArgs& a = p.a;
+  const size_t rows = (size_t)a.q_indptr[a.batch] * a.h_kv * a.group;
+  const size_t all = (size_t)a.n_q * a.h_kv * a.group;
+  const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (at >= rows || at >= all) return;
+  float m = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[s * all + at]);
+  m = warp_max(m);
+  constexpr int E = D / 32;
+  float o[E] = {}, sum = 0.f;
+  if (m != -INFINITY) {
+    for (int s = 0; s < p.splits; ++s) {
+      const float w = ex2(p.part_lse[s * all + at] - m);
+      sum += w;
+      const float* src = p.part_o + (s * all + at) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  __half2* dst = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = __floats2half2_rn(o[e] * inv, o[e + 1] * inv);
+  if (lane == 0 && a.lse) a.lse[at] = sum > 0.f ? (m + lg2(sum)) * LN2 : -INFINITY;
+}
+
+template <int D, int TILES>
+cudaError_t launch_prefill_mma_t(const PrefillMaps& maps, const PrefillArgs& p, cudaStream_t s) {
+  using P = PrefillShape<D, TILES>;
+  const unsigned grid = (unsigned)p.blocks * p.a.h_kv * p.splits;
+  auto go = [&](auto kernel) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, P::THREADS, P::SMEM, s>>>(maps, p);
+    return cudaGetLastError();
+  };
+  const bool cap = p.a.softcap > 0.f, alibi = p.a.slopes != nullptr;
+  cudaError_t e = cap ? (alibi ? go(prefill_mma_kernel<D, TILES, true, true>)
+                               : go(prefill_mma_kernel<D, TILES, true, false>))
+                      : (alibi ? go(prefill_mma_kernel<D, TILES, false, true>)
+                               : go(prefill_mma_kernel<D, TILES, false, false>));
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const size_t rows = (size_t)p.a.n_q * p.a.h_kv * p.a.group;
+  prefill_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace quest
