@@ -468,15 +468,15 @@ typedef struct quest_score_mods {
  * its visible keys (the dense layers of Quest page §1 and §1.2), read through
  * the page table itself: no scores, no selection lists. The query's position
  * is seq_lens[r] - 1 (pages->seq_lens includes the new token). The (KV head,
- * page) items of all requests are cut into equal runs, one per CTA, whatever
- * the requests' lengths; a row cut over several CTAs is joined by log-sum-exp
- * by the CTA that finishes last, always in the same order.
+ * page) items of all requests are cut into equal runs, one per warp, whatever
+ * the requests' lengths; the parts of a unit that is cut over several runs are
+ * joined by log-sum-exp in a second kernel, always in the same order.
  *   q, group, out, lse, sm_scale : as quest_sparse_decode_attn
  *   mods      : NULL, or as above with one doc_starts entry per request
  *   workspace : device, >= quest_dense_decode_workspace_size(...) bytes, 16-B
- *               aligned, ZERO-FILLED before its first use; a call leaves its
- *               counters at zero again. Calls that share a workspace must not
- *               overlap on the GPU.
+ *               aligned; nothing in it has to be set or kept. Calls that share
+ *               a workspace must not overlap on the GPU.
+ * At most 524288 requests (else QUEST_ERR_UNSUPPORTED).
  * A page outside the pool is skipped (QUEST_DEVERR_PAGE_RANGE), a request's
  * tokens beyond its page table too (QUEST_DEVERR_TABLE_RANGE). Keys and values
  * of the seq_lens[r] valid tokens must be finite, also where a query does not
@@ -509,8 +509,7 @@ QUEST_API size_t quest_dense_decode_workspace_size(int32_t batch, int32_t nnz, i
  *   out      : device dtype [n_q, h_kv * group, head_dim]
  *   lse      : device fp32 [n_q, h_kv * group], or NULL
  *   workspace: device, >= quest_prefill_workspace_size(...) bytes, 16-B
- *              aligned, ZERO-FILLED before its first use; as in
- *              quest_dense_decode_attn
+ *              aligned; as in quest_dense_decode_attn
  * fp16: the products run on the tensor cores with fp32 accumulation, softmax
  * weights rounded to fp16. Errors and finiteness as quest_dense_decode_attn.
  */

@@ -381,28 +381,33 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
 
 
 def _expect(name, t, dtype, shape, device, rows=False):
-    """Raises unless t is a dense tensor of this type, shape and device (with
-    ``rows``, only each row of the first dimension has to be dense)."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    """Raises unless t is a dense tensor of this type, shape and device index
+    (with ``rows``, only each row of the first dimension has to be dense)."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on CUDA device {device}, not {t.device}")
     if not (t.is_contiguous() or
             (rows and t.shape[0] > 1 and t[0].is_contiguous() and t.stride(0) >= t[0].numel())):
         raise ValueError(f"{name} must be contiguous" + (" within its rows" if rows else ""))
 
 
-def _current(cache: PagedCache):
-    dev = cache.k_pool.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache must be on the current CUDA device, not {dev}")
+def _current(cache: PagedCache) -> int:
+    """Index of the current device, which has to hold the cache."""
+    dev = cache.k_pool.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the cache must be on the current CUDA device, not {cache.k_pool.device}")
     return dev
 
 
-def _zeros(n, dev, stream):
-    """A zeroed workspace, filled on the stream that will use it."""
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _scratch(n, dev, stream):
+    """A workspace from the memory of the stream that will use it."""
     with torch.cuda.stream(stream):
-        return torch.zeros(max(n, 16), dtype=torch.uint8, device=dev)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
 
 
 def _row_stride(t) -> int:
@@ -438,7 +443,7 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
         ctypes.byref(cache.c), ctypes.byref(table.c), ctypes.byref(rope), _ptr(q), _ptr(k_new),
         _ptr(v_new), 0 if q is None else _row_stride(q), _row_stride(k_new), _row_stride(v_new),
         int(n), int(group), _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out),
-        _stream(stream)))
+        _raw_stream(stream, dev)))
     return q_out
 
 
@@ -473,7 +478,7 @@ def dense_decode_attn(cache: PagedCache, table: PageTable, q, group: int, out=No
                       stream=None):
     """quest_dense_decode_attn: (out [B, h_q, d] fp32, lse [B, h_q] fp32) of one
     query per request over all of its cached tokens. ``workspace``: uint8,
-    dense_decode_workspace_size bytes, zero-filled before its first use."""
+    dense_decode_workspace_size bytes."""
     dev, h_q, d = _current(cache), cache.h_kv * group, cache.head_dim
     B = table.batch
     _expect("q", q, cache.dtype, (B, h_q, d), dev)
@@ -488,11 +493,11 @@ def dense_decode_attn(cache: PagedCache, table: PageTable, q, group: int, out=No
     if workspace is None:
         n = dense_decode_workspace_size(B, table.nnz, cache.h_kv, group, d, cache.page_size,
                                         cache.dtype)
-        workspace = _zeros(n, dev, stream)
+        workspace = _scratch(n, dev, stream)
     _check(lib().quest_dense_decode_attn(
         ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q), int(group),
         None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
-        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _stream(stream)))
+        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _raw_stream(stream, dev)))
     return out, lse
 
 
@@ -507,7 +512,7 @@ def prefill_attn(cache: PagedCache, table: PageTable, q, group: int, q_indptr, o
     """quest_prefill_attn: (out [n_q, h_q, d] in the cache's type, lse [n_q, h_q]
     fp32) of each request's last tokens, rows q_indptr[r] .. q_indptr[r + 1] of
     q, over its cached tokens. ``workspace``: uint8, prefill_workspace_size
-    bytes, zero-filled before its first use."""
+    bytes."""
     dev, h_q, d = _current(cache), cache.h_kv * group, cache.head_dim
     n = q.shape[0]
     _expect("q", q, cache.dtype, (n, h_q, d), dev)
@@ -523,11 +528,11 @@ def prefill_attn(cache: PagedCache, table: PageTable, q, group: int, q_indptr, o
     if workspace is None:
         size = prefill_workspace_size(table.batch, n, table.nnz, cache.h_kv, group, d,
                                       cache.page_size, cache.dtype)
-        workspace = _zeros(size, dev, stream)
+        workspace = _scratch(size, dev, stream)
     _check(lib().quest_prefill_attn(
         ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q), int(group), _ptr(q_indptr), int(n),
         None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
-        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _stream(stream)))
+        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _raw_stream(stream, dev)))
     return out, lse
 
 

@@ -28,7 +28,8 @@ SOURCES = ["quest_api.cu", "append.cu", "score.cu", "select.cu", "attn.cu", "ste
            "prefill_f16_d128_t2.cu"]
 SHARED_HEADERS = ("common.cuh", "internal.h")
 STEP_HEADERS = ("topk.cuh", "attn_dev.cuh", "attn_mma.cuh", "step_impl.cuh", "cstep_impl.cuh")
-DENSE_HEADERS = ("dense.h", "dense.cuh", "dense_rows.cuh", "tc.cuh", "prefill_mma.cuh")
+DENSE_HEADERS = ("dense.h", "dense.cuh", "dense_rows.cuh", "tc.cuh", "tmap.h",
+                 "prefill_mma.cuh", "dense_decode.cuh", "attn_mma.cuh")
 
 
 def headers_of(src):

@@ -39,6 +39,7 @@ struct DenseArgs {
   float scale;
   unsigned* err;
 };
+constexpr int32_t kDecodeMaxBatch = 1 << 19;  // its running sums stay in shared memory
 size_t dense_decode_workspace(int32_t batch, int32_t nnz, int32_t h_kv, int32_t group,
                               int32_t head_dim, int32_t page_size, int32_t dtype);
 cudaError_t launch_dense_decode(const DenseArgs& a, cudaStream_t s);

@@ -97,7 +97,9 @@ quest_status quest_rope_append_kv(const quest_cache* cache, const quest_pages* p
 
 size_t quest_dense_decode_workspace_size(int32_t batch, int32_t nnz, int32_t h_kv, int32_t group,
                                          int32_t head_dim, int32_t page_size, int32_t dtype) {
-  if (batch <= 0 || nnz < 0 || !valid_shape(h_kv, group, head_dim, page_size, dtype)) return 0;
+  if (batch <= 0 || batch > quest::kDecodeMaxBatch || nnz < 0 ||
+      !valid_shape(h_kv, group, head_dim, page_size, dtype))
+    return 0;
   return quest::dense_decode_workspace(batch, nnz, h_kv, group, head_dim, page_size, dtype);
 }
 
@@ -111,6 +113,7 @@ quest_status quest_dense_decode_attn(const quest_cache* cache, const quest_pages
   if (!valid_group(group)) return QUEST_ERR_UNSUPPORTED;
   if ((st = check_mods(mods)) != QUEST_OK) return st;
   if (pages->batch == 0) return QUEST_OK;
+  if (pages->batch > quest::kDecodeMaxBatch) return QUEST_ERR_UNSUPPORTED;
   if (!q || !out || !aligned16(q) || !aligned16(out)) return QUEST_ERR_INVALID_ARG;
   const size_t need = quest::dense_decode_workspace(pages->batch, pages->nnz, cache->h_kv, group,
                                                     cache->head_dim, cache->page_size, cache->dtype);

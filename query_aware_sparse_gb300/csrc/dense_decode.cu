@@ -1,22 +1,73 @@
-// Dense decode attention: one query row per request over its paged cache.
-#include "dense_rows.cuh"
+// Dense decode attention: plan, tensor maps and launch (dense_decode.cuh).
+#include "dense_decode.cuh"
+#include "internal.h"
+#include "tmap.h"
 
 namespace quest {
+namespace {
 
-size_t dense_decode_workspace(int32_t, int32_t, int32_t, int32_t, int32_t, int32_t, int32_t) {
-  return 16;
+struct Plan { int warps; size_t part_o, part_ml, bytes; };
+
+Plan plan_decode(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim) {
+  Plan p;
+  p.warps = sm_count() * kDecodeWarps;
+  const size_t slots = ((size_t)p.warps + (size_t)batch * h_kv) * group;
+  p.part_o = (((size_t)batch + 1) * sizeof(long long) + 255) & ~(size_t)255;
+  p.part_ml = p.part_o + slots * head_dim * sizeof(float);
+  p.bytes = p.part_ml + slots * sizeof(float2);
+  return p;
+}
+
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename W, int D>
+cudaError_t launch(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) {
+  using Sh = DecodeShape<typename W::T, D>;
+  cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel<W, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(dense_decode_kernel<W, D>, p.n_warps / kDecodeWarps, kDecodeWarps * 32, Sh::SMEM, s, maps, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, 128, 0, s, p);
+}
+
+}  // namespace
+
+size_t dense_decode_workspace(int32_t batch, int32_t, int32_t h_kv, int32_t group,
+                              int32_t head_dim, int32_t, int32_t) {
+  return plan_decode(batch, h_kv, group, head_dim).bytes;
 }
 
 cudaError_t launch_dense_decode(const DenseArgs& a, cudaStream_t s) {
-  const dim3 grid(a.batch, a.h_kv * a.group);
-  if (a.dtype == QUEST_F16) {
-    if (a.head_dim == 128) dense_rows_kernel<__half, float, 128><<<grid, kRowThreads, 0, s>>>(a);
-    else dense_rows_kernel<__half, float, 64><<<grid, kRowThreads, 0, s>>>(a);
-  } else {
-    if (a.head_dim == 128) dense_rows_kernel<float, float, 128><<<grid, kRowThreads, 0, s>>>(a);
-    else dense_rows_kernel<float, float, 64><<<grid, kRowThreads, 0, s>>>(a);
-  }
-  return cudaGetLastError();
+  const Plan plan = plan_decode(a.batch, a.h_kv, a.group, a.head_dim);
+  char* ws = static_cast<char*>(a.workspace);
+  DecodeArgs p{};
+  p.a = a;
+  p.starts = reinterpret_cast<long long*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  p.n_warps = plan.warps;
+  p.wait_limit = wait_limit();
+  DecodeMaps maps;
+  const int rows = a.dtype == QUEST_F16 ? 16 : 8;
+  if (!encode_pool(&maps.k, a, a.k_pool, rows) || !encode_pool(&maps.v, a, a.v_pool, rows))
+    return cudaErrorInvalidValue;
+  if (a.dtype == QUEST_F16)
+    return a.head_dim == 128 ? launch<WarpF16<128>, 128>(maps, p, s) : launch<WarpF16<64>, 64>(maps, p, s);
+  return a.head_dim == 128 ? launch<WarpF32<128>, 128>(maps, p, s) : launch<WarpF32<64>, 64>(maps, p, s);
 }
 
 }  // namespace quest

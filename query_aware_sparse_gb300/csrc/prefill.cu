@@ -3,6 +3,7 @@
 #include "dense_rows.cuh"
 #include "internal.h"
 #include "prefill_mma.cuh"
+#include "tmap.h"
 
 namespace quest {
 
@@ -20,14 +21,6 @@ struct Plan {
   int tiles, blocks, splits;
   size_t lse_at, bytes;               // of the partial results in the workspace
 };
-
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  cudaGetLastError();
-  return sms;
-}
 
 Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
                   int32_t head_dim, int32_t page_size, int32_t dtype) {
@@ -55,33 +48,6 @@ Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t
   return p;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-  static const EncodeTiled f = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<EncodeTiled>(fn);
-  }();
-  return f;
-}
-
-bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box) {
-  const cuuint32_t one[3] = {1, 1, 1};
-  const EncodeTiled f = encoder();
-  return f && f(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base), dims, strides,
-                box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t launch_f16(const DenseArgs& a, cudaStream_t s) {
   const Plan plan = plan_prefill(a.batch, a.n_q, a.nnz, a.h_kv, a.group, a.head_dim, a.page_size, a.dtype);
   PrefillArgs p{};
@@ -97,11 +63,8 @@ cudaError_t launch_f16(const DenseArgs& a, cudaStream_t s) {
   const cuuint64_t q_dims[3] = {d, hq, (cuuint64_t)a.n_q}, q_strides[2] = {d * 2, hq * d * 2};
   const cuuint32_t q_box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(128 / a.group)};
   // pools: a box is one page of one KV head, 64 dims
-  const cuuint64_t p_dims[2] = {d, (cuuint64_t)a.n_phys * a.h_kv * a.page_size}, p_strides[1] = {d * 2};
-  const cuuint32_t p_box[2] = {64, (cuuint32_t)a.page_size};
-  if (!encode(&maps.q, a.q, 3, q_dims, q_strides, q_box) ||
-      !encode(&maps.k, a.k_pool, 2, p_dims, p_strides, p_box) ||
-      !encode(&maps.v, a.v_pool, 2, p_dims, p_strides, p_box))
+  if (!encode_map(&maps.q, a.dtype, a.q, 3, q_dims, q_strides, q_box) ||
+      !encode_pool(&maps.k, a, a.k_pool, a.page_size) || !encode_pool(&maps.v, a, a.v_pool, a.page_size))
     return cudaErrorInvalidValue;
   if (a.head_dim == 128)
     return plan.tiles == 2 ? launch_prefill_f16_d128_t2(maps, p, s) : launch_prefill_f16_d128_t1(maps, p, s);

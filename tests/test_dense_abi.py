@@ -109,6 +109,7 @@ def test_attention_refuses_arguments(q):
         assert f(ws=None) == WORKSPACE and f(ws=FAKE + 8) == WORKSPACE and f(size=0) == WORKSPACE
         assert f(pages=_pages(q, seq=None)) == INVALID
     assert pre(ind=None) == INVALID and pre(n=-1) == INVALID
+    assert dec(pages=_pages(q, batch=(1 << 19) + 1)) == UNSUPPORTED
 
 
 def test_empty_calls_are_no_ops(q):
@@ -146,7 +147,7 @@ def test_binding_refuses_tensors(q):
         q.prefill_attn(cache, table, x, 1, i32)
     with pytest.raises(ValueError, match="current CUDA device"):
         q.rope_append_kv(cache, table, x, x, x, i32, i32[:1], torch.ones(32, dtype=torch.float64), 1)
-    dev = x.device
+    dev = x.get_device()
     q._expect("x", x, torch.float16, (1, 2, 64), dev)
     for bad in (x.float(), x[0], x.expand(3, 2, 64)):
         with pytest.raises(ValueError, match="x must be"):
