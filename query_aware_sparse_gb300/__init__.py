@@ -387,9 +387,10 @@ def _expect(name, t, dtype, shape, device, rows=False):
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} must be on CUDA device {device}, not {t.device}")
-    if not (t.is_contiguous() or
-            (rows and t.shape[0] > 1 and t[0].is_contiguous() and t.stride(0) >= t[0].numel())):
-        raise ValueError(f"{name} must be contiguous" + (" within its rows" if rows else ""))
+    if not t.is_contiguous():
+        s, d = t.stride(), t.shape[-1]
+        if not rows or t.shape[0] == 1 or s[2] != 1 or s[1] != d or s[0] < t.shape[1] * d:
+            raise ValueError(f"{name} must be contiguous" + (" within its rows" if rows else ""))
 
 
 def _current(cache: PagedCache) -> int:

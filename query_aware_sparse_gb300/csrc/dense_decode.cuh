@@ -92,8 +92,19 @@ template <int D> struct WarpF16 {
   using T = __half;
   static constexpr int KT = D / 16;
   uint32_t qb[KT][2];
-  float m[2], l[2], acc[KT][4];
+  float m[2], l[2], acc[KT][4], sum[KT][4];
   float slope2[2];
+  int since;                // tiles in acc
+
+  // The tensor core's accumulation truncates: a long chain would lose a bit
+  // per doubling, always downwards. acc takes eight tiles, then goes to sum.
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) { sum[k][c] += acc[k][c]; acc[k][c] = 0.f; }
+    since = 0;
+  }
 
   __device__ __forceinline__ void begin(const DenseArgs& a, int r, int g, int lane, float*) {
     const int head = lane >> 2, t = lane & 3;
@@ -112,7 +123,8 @@ template <int D> struct WarpF16 {
 #pragma unroll
     for (int k = 0; k < KT; ++k)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[k][c] = 0.f;
+      for (int c = 0; c < 4; ++c) sum[k][c] = acc[k][c] = 0.f;
+    since = 0;
   }
 
   // tokens tok0 .. tok0 + 15 of the tile in shared memory at k_s and v_s
@@ -152,6 +164,7 @@ template <int D> struct WarpF16 {
     }
     float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
     if (__any_sync(FULL, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+      settle();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -161,7 +174,7 @@ template <int D> struct WarpF16 {
           m[i] = mx[i];
           l[i] *= f;
 #pragma unroll
-          for (int k = 0; k < KT; ++k) { acc[k][i] *= f; acc[k][2 + i] *= f; }
+          for (int k = 0; k < KT; ++k) { sum[k][i] *= f; sum[k][2 + i] *= f; }
         }
       }
     }
@@ -197,12 +210,14 @@ template <int D> struct WarpF16 {
       mma_f16_16816(acc[k], a0, a1, a2, a3, hi[0], hi[1]);
       mma_f16_16816(acc[k], a0, a1, a2, a3, lo[0], lo[1]);
     }
+    if (++since == 8) settle();
   }
 
   // The state as o (times `whole ? 1 / l : 1`), m and l of head i, dims 16 k + ..
   template <typename F>
   __device__ __forceinline__ void finish(const DenseArgs& a, bool whole, int lane, F put) {
     const int t = lane & 3;
+    settle();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -213,8 +228,8 @@ template <int D> struct WarpF16 {
         float* o = put(head, m[i], l[i], (lane >> 2) == 0);
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-          o[16 * k + (lane >> 2)] = acc[k][i] * f;
-          o[16 * k + (lane >> 2) + 8] = acc[k][2 + i] * f;
+          o[16 * k + (lane >> 2)] = sum[k][i] * f;
+          o[16 * k + (lane >> 2) + 8] = sum[k][2 + i] * f;
         }
       }
     }

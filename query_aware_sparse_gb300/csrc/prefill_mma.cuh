@@ -51,8 +51,7 @@ template <int D, int TILES> struct PrefillShape {
   static constexpr uint32_t Q_TILE = 128 * D * 2, BLOCK = BN * D * 2;
   static constexpr int STAGES = TILES == 2 ? (D == 128 ? 5 : 8) : (D == 128 ? 4 : 8);
   static constexpr uint32_t SMEM = 1024 + TILES * Q_TILE + STAGES * BLOCK;
-  static constexpr int THREADS = TILES * 128 + 64;
-  static constexpr int BOUND = TILES * 128 + 128;      // registers come in fours of warps
+  static constexpr int THREADS = TILES * 128 + 128;    // the last four warps: load, issue, two idle
   static constexpr uint32_t O_COL = TILES * SBUF * BN;         // S buffers first
   static constexpr uint32_t TMEM = O_COL + TILES * D <= 128 ? 128 : O_COL + TILES * D <= 256 ? 256 : 512;
   static constexpr int PER_SM = TILES == 2 ? 1 : 2;
@@ -85,7 +84,7 @@ __device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int i
 }
 
 template <int D, int TILES, bool CAP, bool ALIBI>
-__global__ void __launch_bounds__(PrefillShape<D, TILES>::BOUND, PrefillShape<D, TILES>::PER_SM)
+__global__ void __launch_bounds__(PrefillShape<D, TILES>::THREADS, PrefillShape<D, TILES>::PER_SM)
 prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p) {
   using P = PrefillShape<D, TILES>;
   constexpr int BN = P::BN, SBUF = P::SBUF, HALVES = P::HALVES, STAGES = P::STAGES;
@@ -195,8 +194,10 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   const uint32_t ring = q_s + TILES * P::Q_TILE;
   const int pages_per_block = BN / S;
 
+  // two tiles: 384 threads of 168 registers, 256 x 208 + 128 x 80 = 63488 of 64512
   if (warp == 4 * TILES) {
     // ---- loads ----------------------------------------------------------------
+    if (TILES == 2) regs_down<80>();
     if (n1 > n0 && lane == 0) {
       mbar_expect_tx(&q_full, TILES * P::Q_TILE);
 #pragma unroll
@@ -271,6 +272,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     }
   } else if (warp == 4 * TILES + 1) {
     // ---- tensor core -------------------------------------------------------------
+    if (TILES == 2) regs_down<80>();
     if (lane == 0 && n1 > n0) {
       constexpr uint32_t ID_S = mma_idesc(128, BN, false), ID_O = mma_idesc(128, D, true);
       // stage of K of block n is 2 (n - n0) of the ring's sequence, V the next
@@ -340,8 +342,9 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       mma_commit(smem_u32(&drain));
       for (uint32_t k = 0; k < p.wait_limit && !mbar_try_wait_sleep(&drain, 0, 1000u); ++k) {}
     }
-  } else {
+  } else if (softmax_warp) {
     // ---- softmax: one row per thread ------------------------------------------------
+    if (TILES == 2) regs_up<208>();
     const int row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
     const int h = g * G + row % G;
@@ -392,9 +395,13 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
         for (int c = 0; c < BN; ++c)
           if (kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1)) x[c] = -INFINITY;
       }
-      float mx = x[0];
+      float mc[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 1; c < BN; ++c) mx = fmaxf(mx, x[c]);
+      for (int c = 4; c < BN; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mc[e] = c + 4 < BN ? fmaxf(fmaxf(mc[e], x[c + e]), x[c + 4 + e]) : fmaxf(mc[e], x[c + e]);
+      float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
       mx *= sl2;
       const bool grow = mx > m + 8.f;                 // also the first finite maximum
       if (__any_sync(FULL, grow)) {
@@ -418,22 +425,23 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
         if (grow) m = mx;
       }
       const float mu = m == -INFINITY ? 0.f : m - 6.f;
-      float sum0 = 0.f, sum1 = 0.f;
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float2 sl = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
 #pragma unroll
       for (int c = 0; c < BN / 64; ++c) {
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float pa = ex2(fmaf(x[c * 64 + 2 * e], sl2, -mu));
-          const float pb = ex2(fmaf(x[c * 64 + 2 * e + 1], sl2, -mu));
-          sum0 += pa;
-          sum1 += pb;
-          const __half2 hh = __floats2half2_rn(pa, pb);
+          float2 v = make_float2(x[c * 64 + 2 * e], x[c * 64 + 2 * e + 1]);
+          v = fma2(v, sl, nmu);
+          v = make_float2(ex2(v.x), ex2(v.y));
+          sum[e & 1] = add2(sum[e & 1], v);
+          const __half2 hh = __floats2half2_rn(v.x, v.y);
           w[e] = *reinterpret_cast<const uint32_t*>(&hh);
         }
         tmem_st32(s_col + c * 32, w);
       }
-      l += sum0 + sum1;
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_wait_st();
       // the last block's product: done by now, and a wait on the next phase
       // would pass at once while this one is open
@@ -487,6 +495,8 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
         else if (a.lse) a.lse[at] = lse2 * LN2;
       }
     }
+  } else if (TILES == 2) {
+    regs_down<80>();
   }
   tc_fence_before();
   __syncthreads();

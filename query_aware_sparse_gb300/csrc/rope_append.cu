@@ -195,10 +195,11 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
   const int ntok = min(t_end - t_begin, a.n_new - row0);
   const int half = a.rotary_dim / 2;
 
-  for (int i = threadIdx.x; i < ntok * half; i += kThreads) {
-    const int t = i / half, jj = i - t * half;
+  // a thread keeps its pair through the tokens: one 64-bit division of the turn
+  const int jj = threadIdx.x % half;
+  const unsigned long long f = turn_fraction(a.inv_freq[jj]);
+  for (int t = threadIdx.x / half; t < ntok && threadIdx.x < kThreads / half * half; t += kThreads / half) {
     const int p = a.positions ? a.positions[row0 + t] : t_begin + t;
-    const unsigned long long f = turn_fraction(a.inv_freq[jj]);
     const int turn = (int)(((unsigned long long)(long long)p * f) >> 32);   // half turns in 2^-31
     float sn, cs;
     sincospif((float)turn * 0x1p-31f, &sn, &cs);
