@@ -3,10 +3,12 @@
 // Mathematics. For a block of query rows (the tokens of one request times the
 // group's heads, head fastest) and one KV head: over blocks of BN keys
 //   S = Q K^T;  x = mods(S) in base 2, -inf where a row does not see the key;
-//   m' = max(m, max x);  P = 2^(x - m' + 6);  l += sum P;  O += P V
-// and O / l at the end. The running maximum is let lag behind by up to 2^8
-// before O is rescaled, so rescaling is rare; the factor 2^6 keeps small
-// weights out of fp16's subnormal range (P < 2^14). P is rounded to fp16 (half
+//   P = 2^(x - m + 6);  l += sum P;  O += P V
+// and O / l at the end. m is a maximum of the row so far, but not taken for
+// every block: it stays until a row's weights of a block sum to more than 2^15
+// (then m is renewed, O and l rescaled, the block's weights done again). The
+// usual block so needs no maximum at all, and no weight passes fp16's 65504;
+// the factor 2^6 keeps small weights out of fp16's subnormal range. P is rounded to fp16 (half
 // a step, 2^-11 of itself) because the second product takes fp16 operands;
 // S, O, m and l stay in fp32.
 //
@@ -90,13 +92,13 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   constexpr int BN = P::BN, SBUF = P::SBUF, HALVES = P::HALVES, STAGES = P::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t q_full, full[STAGES], empty[STAGES], aux, drain;
-  __shared__ __align__(8) uint64_t s_full[TILES][SBUF], p_full[TILES][SBUF], pv_done[TILES];
+  __shared__ __align__(8) uint64_t s_full[TILES][SBUF], p_full[TILES][SBUF], pv_done[TILES], o_full[TILES];
   __shared__ uint32_t s_tmem;
   __shared__ int s_req, s_blk, s_lo[TILES], s_hi[TILES], s_bad;
   __shared__ volatile int s_quit;
 
   const DenseArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.group, S = a.page_size, hq = a.h_kv * G;
   const int page_shift = S == 16 ? 4 : 5;
   const int tile_tokens = 128 / G, block_tokens = TILES * tile_tokens;
@@ -125,8 +127,9 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     mbar_init(&drain, 1);
     for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int t = 0; t < TILES; ++t) {
-      for (int i = 0; i < SBUF; ++i) { mbar_init(&s_full[t][i], 1); mbar_init(&p_full[t][i], 128); }
+      for (int i = 0; i < SBUF; ++i) { mbar_init(&s_full[t][i], 1); mbar_init(&p_full[t][i], 4); }
       mbar_init(&pv_done[t], 1);
+      mbar_init(&o_full[t], 1);
     }
     fence_mbar_init();
   }
@@ -195,10 +198,12 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   const int pages_per_block = BN / S;
 
   // two tiles: 384 threads of 168 registers, 256 x 208 + 128 x 80 = 63488 of 64512
-  if (warp == 4 * TILES) {
-    // ---- loads ----------------------------------------------------------------
+  if (warp == 4 * TILES || warp == 4 * TILES + 2) {
+    // ---- loads: one warp the K blocks and Q, another the V blocks ---------------
     if (TILES == 2) regs_down<80>();
-    if (n1 > n0 && lane == 0) {
+    const int kv = warp == 4 * TILES ? 0 : 1;
+    const CUtensorMap* map = kv ? &maps.v : &maps.k;
+    if (kv == 0 && n1 > n0 && lane == 0) {
       mbar_expect_tx(&q_full, TILES * P::Q_TILE);
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
@@ -208,8 +213,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
                  row0 + tok0 + t * tile_tokens, smem_u32(&q_full));
     }
     const int held_pages = (held + S - 1) / S;
-    int stage = 0, done = 0;                          // stages filled so far
-    uint32_t phase = 0, aux_phase = 0;
+    uint32_t aux_phase = 0;
     bool go = true;
     auto page_of = [&](int n) {
       const int lp = n * pages_per_block + lane;
@@ -217,129 +221,132 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       if (lane < pages_per_block && n < n1 && lp < held_pages) id = a.page_indices[e0 + lp];
       return id >= 0 && id < a.n_phys ? id : -1;
     };
-    int id = page_of(n0);
-    for (int n = n0; go && n < n1; ++n) {
+    int id = page_of(n0), seq = kv;                    // block seq of the ring's sequence
+    for (int n = n0; n < n1; ++n, seq += 2) {
       const int next = page_of(n + 1);
       const unsigned have = __ballot_sync(FULL, id >= 0);
       const uint32_t bytes = __popc(have) * S * D * 2;
       const bool ragged = held < (n + 1) * BN || __popc(have) < pages_per_block;
       const int y = id >= 0 ? (id * a.h_kv + g) * S : 0;
+      const int stage = seq % STAGES;
+      if (seq >= STAGES &&
+          !(go = warp_wait_or_quit(&empty[stage], (seq / STAGES & 1) ^ 1, p.wait_limit, &s_quit)))
+        break;
+      const uint32_t dst = ring + stage * P::BLOCK;
+      uint64_t* bar = kv && ragged ? &aux : &full[stage];
+      if (lane == 0 && bytes) mbar_expect_tx(bar, bytes);
+      __syncwarp();
+      if (id >= 0) {
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (done >= STAGES && !warp_wait_or_quit(&empty[stage], phase ^ 1, p.wait_limit, &s_quit)) {
-          go = false;
-          break;
+        for (int h = 0; h < HALVES; ++h)
+          tma_2d(dst + h * BN * 128 + lane * S * 128, map, h * 64, y, smem_u32(bar));
+      }
+      __syncwarp();
+      if (kv && ragged) {
+        // zero what is no valid token, then hand the block over
+        if (bytes) {
+          if (!(go = warp_wait_or_quit(&aux, aux_phase, p.wait_limit, &s_quit))) break;
+          aux_phase ^= 1;
         }
-        const uint32_t dst = ring + stage * P::BLOCK;
-        uint64_t* bar = kv && ragged ? &aux : &full[stage];
-        if (lane == 0 && bytes) mbar_expect_tx(bar, bytes);
-        __syncwarp();
-        if (id >= 0) {
-#pragma unroll
-          for (int h = 0; h < HALVES; ++h)
-            tma_2d(dst + h * BN * 128 + lane * S * 128, kv ? &maps.v : &maps.k, h * 64, y,
-                   smem_u32(bar));
-        }
-        __syncwarp();
-        if (kv && ragged) {
-          // zero what is no valid token, then hand the block over
-          if (bytes) {
-            if (!warp_wait_or_quit(&aux, aux_phase, p.wait_limit, &s_quit)) { go = false; break; }
-            aux_phase ^= 1;
+        for (int i = lane; i < BN * HALVES * 8; i += 32) {
+          const int row = i >> 3 & (BN - 1), h = i / (8 * BN);
+          if (n * BN + row >= held || !(have >> (row >> page_shift) & 1)) {
+            const uint32_t at = dst + h * BN * 128 + row * 128 + (i & 7) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" :: "r"(at), "r"(0) : "memory");
           }
-          for (int i = lane; i < BN * HALVES * 8; i += 32) {
-            const int row = i >> 3 & (BN - 1), h = i / (8 * BN);
-            if (n * BN + row >= held || !(have >> (row >> page_shift) & 1)) {
-              const uint32_t at = dst + h * BN * 128 + row * 128 + (i & 7) * 16;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" :: "r"(at), "r"(0) : "memory");
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[stage]);
-        } else if (!bytes && lane == 0) {
-          mbar_arrive(&full[stage]);
         }
-        ++done;
-        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+      } else if (!bytes && lane == 0) {
+        mbar_arrive(&full[stage]);
       }
       id = next;
     }
-    if (s_quit) {                                     // wait (bounded) for the copies in flight
-      for (int i = 0; i < STAGES && i < done; ++i)
-        for (uint32_t k = 0; k < p.wait_limit && !mbar_try_wait_sleep(&full[i], (done - 1 - i) / STAGES & 1, 1000u); ++k) {}
-      for (uint32_t k = 0; k < p.wait_limit && n1 > n0 && !mbar_try_wait_sleep(&q_full, 0, 1000u); ++k) {}
+    if (s_quit) {                                      // wait (bounded) for the copies in flight
+      for (int k = seq - 2; k >= 0 && k > seq - 2 - STAGES; k -= 2)
+        for (uint32_t i = 0; i < p.wait_limit && !mbar_try_wait_sleep(&full[k % STAGES], k / STAGES & 1, 1000u); ++i) {}
+      for (uint32_t i = 0; i < p.wait_limit && kv == 0 && n1 > n0 && !mbar_try_wait_sleep(&q_full, 0, 1000u); ++i) {}
     }
   } else if (warp == 4 * TILES + 1) {
-    // ---- tensor core -------------------------------------------------------------
+    // ---- tensor core: the warp stays converged, one lane issues ------------------
     if (TILES == 2) regs_down<80>();
-    if (lane == 0 && n1 > n0) {
+    const int blocks = __shfl_sync(FULL, n1 - n0, 0);
+    // active block ranges of the tiles, counted from n0
+    const int a0 = __shfl_sync(FULL, t0[0] - n0, 0), b0 = __shfl_sync(FULL, t1[0] - n0, 0);
+    const int a1 = __shfl_sync(FULL, t0[TILES - 1] - n0, 0), b1 = __shfl_sync(FULL, t1[TILES - 1] - n0, 0);
+    const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+    const uint32_t lead = elect_one();
+    if (blocks > 0) {
       constexpr uint32_t ID_S = mma_idesc(128, BN, false), ID_O = mma_idesc(128, D, true);
-      // stage of K of block n is 2 (n - n0) of the ring's sequence, V the next
-      auto stage_of = [&](int seq) { return seq % STAGES; };
-      auto issue_s = [&](int t, int n) {
-        const int seq = 2 * (n - n0);
-        const uint32_t k_s = ring + stage_of(seq) * P::BLOCK, a_s = q_s + t * P::Q_TILE;
-        const int buf = SBUF == 2 ? (n - n0) & 1 : 0;
+      const uint64_t q_d = smem_desc(q_s, 16, 1024), k_d = smem_desc(ring, 16, 1024);
+      const uint64_t v_d = smem_desc(ring, BN * 128, 1024);
+      auto active = [&](int t, int n) { return t == 0 ? n >= a0 && n < b0 : n >= a1 && n < b1; };
+      auto issue_s = [&](int t, int buf, int stage) {
+        const uint64_t qd = q_d + t * (P::Q_TILE >> 4), kd = k_d + stage * (P::BLOCK >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t in = (k & 3) * 32;
-          mma_ss(tmem + (t * SBUF + buf) * BN, smem_desc(a_s + (k >> 2) * 128 * 128 + in, 16, 1024),
-                 smem_desc(k_s + (k >> 2) * BN * 128 + in, 16, 1024), ID_S, k > 0);
-        }
-        mma_commit(smem_u32(&s_full[t][buf]));
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(lead, tm + (t * SBUF + buf) * BN, qd + ((k >> 2) * 128 * 128 + (k & 3) * 32 >> 4),
+                 kd + ((k >> 2) * BN * 128 + (k & 3) * 32 >> 4), ID_S, k > 0);
+        mma_commit(lead, &s_full[t][buf]);
       };
-      auto wait_full = [&](int seq) {
-        return wait_or_quit(&full[stage_of(seq)], (seq / STAGES) & 1, p.wait_limit, &s_quit);
+      auto issue_o = [&](int t, int buf, int stage, bool acc) {
+        const uint64_t vd = v_d + stage * (P::BLOCK >> 4);
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          mma_ts(lead, tm + P::O_COL + t * D, tm + (t * SBUF + buf) * BN + k * 8, vd + (k * 2048 >> 4),
+                 ID_O, acc || k > 0);
       };
-      auto active = [&](int t, int n) {
-        return t == 0 ? n >= t0[0] && n < t1[0] : n >= t0[TILES - 1] && n < t1[TILES - 1];
-      };
-      bool go = wait_or_quit(&q_full, 0, p.wait_limit, &s_quit) && wait_full(0);
-      uint32_t p_phase = 0;                           // a bit per S buffer
-      if (go) {
+      // places of the ring: K of block n, then V of it, then K of block n + 1
+      int ks = 0, vs = 1;
+      uint32_t kp = 0, vp = 0, p_phase = 0;           // their phases; a bit per S buffer
+      auto k_next = [&]() { ks += 2; if (ks >= STAGES) { ks -= STAGES; kp ^= 1; } };
+      auto v_next = [&]() { vs += 2; if (vs >= STAGES) { vs -= STAGES; vp ^= 1; } };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = warp_wait_or_quit(bar, parity, p.wait_limit, &s_quit);
         tc_fence_after();
+        return ok;
+      };
+      bool go = wait(&q_full, 0) && wait(&full[0], 0);
+      if (go) {
+#pragma unroll
         for (int t = 0; t < TILES; ++t)
-          if (active(t, n0)) issue_s(t, n0);
-        mma_commit(smem_u32(&empty[0]));
+          if (active(t, 0)) issue_s(t, 0, 0);
+        mma_commit(lead, &empty[0]);
+        k_next();
       }
-      for (int n = n0; go && n < n1; ++n) {
-        const int seq = 2 * (n - n0);
-        const int buf = SBUF == 2 ? (n - n0) & 1 : 0;
-        if (SBUF == 2 && n + 1 < n1) {                // the next S while this softmax runs
-          if (!(go = wait_full(seq + 2))) break;
-          tc_fence_after();
-          for (int t = 0; t < TILES; ++t)
-            if (active(t, n + 1)) issue_s(t, n + 1);
-          mma_commit(smem_u32(&empty[stage_of(seq + 2)]));
+      for (int n = 0; go && n < blocks; ++n) {
+        const int buf = SBUF == 2 ? n & 1 : 0;
+        const bool more = n + 1 < blocks;
+        if (SBUF == 2 && more) {                      // the next S while this softmax runs
+          if (!(go = wait(&full[ks], kp))) break;
+          if (active(0, n + 1)) issue_s(0, buf ^ 1, ks);
+          mma_commit(lead, &empty[ks]);
+          k_next();
         }
-        if (!(go = wait_full(seq + 1))) break;
-        for (int t = 0; go && t < TILES; ++t) {
+        if (!(go = wait(&full[vs], vp))) break;
+        if (SBUF == 1 && more && !(go = wait(&full[ks], kp))) break;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
           if (active(t, n)) {
             const int bit = t * SBUF + buf;
-            if (!(go = wait_or_quit(&p_full[t][buf], p_phase >> bit & 1, p.wait_limit, &s_quit))) break;
+            if (!(go = wait(&p_full[t][buf], p_phase >> bit & 1))) break;
             p_phase ^= 1u << bit;
-            tc_fence_after();
-            const uint32_t v_s = ring + stage_of(seq + 1) * P::BLOCK;
-#pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              mma_ts(tmem + P::O_COL + t * D, tmem + (t * SBUF + buf) * BN + k * 8,
-                     smem_desc(v_s + k * 2048, BN * 128, 1024), ID_O, n > (t == 0 ? t0[0] : t0[TILES - 1]) || k > 0);
-            mma_commit(smem_u32(&pv_done[t]));
+            issue_o(t, buf, vs, n > (t == 0 ? a0 : a1));
+            if (SBUF == 2) mma_commit(lead, &pv_done[t]);
+            if (n + 1 == (t == 0 ? b0 : b1)) mma_commit(lead, &o_full[t]);
           }
-          if (t == TILES - 1) mma_commit(smem_u32(&empty[stage_of(seq + 1)]));
-          if (SBUF == 1 && n + 1 < n1) {
-            if (t == 0) {
-              if (!(go = wait_full(seq + 2))) break;
-              tc_fence_after();
-            }
-            if (active(t, n + 1)) issue_s(t, n + 1);
-            if (t == TILES - 1) mma_commit(smem_u32(&empty[stage_of(seq + 2)]));
+          if (t == TILES - 1) mma_commit(lead, &empty[vs]);
+          if (SBUF == 1 && more) {
+            if (active(t, n + 1)) issue_s(t, 0, ks);
+            if (t == TILES - 1) mma_commit(lead, &empty[ks]);
           }
         }
+        if (SBUF == 1 && more) k_next();
+        v_next();
       }
       // everything issued is done before the CTA may leave (bounded)
-      mma_commit(smem_u32(&drain));
+      mma_commit(lead, &drain);
       for (uint32_t k = 0; k < p.wait_limit && !mbar_try_wait_sleep(&drain, 0, 1000u); ++k) {}
     }
   } else if (softmax_warp) {
@@ -352,7 +359,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     const float cap2 = a.softcap * LOG2E, to_z = CAP ? 2.f * LOG2E * a.scale / a.softcap : 0.f;
     const float slope2 = ALIBI && valid ? a.slopes[h] * LOG2E : 0.f;
     const float sl2 = CAP || ALIBI ? 1.f : log2s;     // of the value the maximum is taken of
-    float m = -INFINITY, l = 0.f;
+    float m = seen.hi > 0 ? -INFINITY : 0.f, l = 0.f;  // a row that sees nothing needs no maximum
     uint32_t s_phase = 0;                             // a bit per S buffer
     bool ok = true;
     const int first = tile == 0 ? t0[0] : t0[TILES - 1], last = tile == 0 ? t1[0] : t1[TILES - 1];
@@ -395,65 +402,72 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
         for (int c = 0; c < BN; ++c)
           if (kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1)) x[c] = -INFINITY;
       }
-      float mc[4] = {x[0], x[1], x[2], x[3]};
+      // The maximum lags: with it the block's weights, and only where their sum
+      // passes 2^15 (one above 2^14 is among them, or many above 2^8) or a row
+      // has no maximum yet is a new one taken and the weights done again.
+      float sum;
+      bool again = __any_sync(FULL, m == -INFINITY);
+      for (bool once = false;; once = true) {
+        if (again) {
+          float mc[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 4; c < BN; c += 8)
+          for (int c = 4; c < BN; c += 4)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mc[e] = c + 4 < BN ? fmaxf(fmaxf(mc[e], x[c + e]), x[c + 4 + e]) : fmaxf(mc[e], x[c + e]);
-      float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3]));
-      mx *= sl2;
-      const bool grow = mx > m + 8.f;                 // also the first finite maximum
-      if (__any_sync(FULL, grow)) {
-        const float f = grow ? ex2(m - mx) : 1.f;     // m = -inf: O and l are zero, f = 0
-        if (n > first) {
-          if (!(ok = warp_wait_or_quit(&pv_done[tile], (n - 1 - first) & 1, p.wait_limit, &s_quit)))
-            break;
-          tc_fence_after();
+            for (int e = 0; e < 4; ++e) mc[e] = fmaxf(mc[e], x[c + e]);
+          const float mx = fmaxf(m, fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * sl2);
+          const float f = mx > m ? ex2(m - mx) : 1.f;   // m = -inf: O and l are zero, f = 0
+          m = mx;
+          l *= f;
+          if (n > first) {
+            // the products up to block n - 1 are in O: with one S buffer the S
+            // that was waited for came after them, with two it came after n - 2
+            if (SBUF == 2 && !(ok = warp_wait_or_quit(&pv_done[tile], (n - 1 - first) & 1, p.wait_limit, &s_quit)))
+              break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_col + c * 32, o);
-            tmem_wait_ld();
-            tmem_loaded(o);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_col + c * 32, o);
+              tmem_wait_ld();
+              tmem_loaded(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(o_col + c * 32, o);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_col + c * 32, o);
+            }
           }
         }
-        l *= f;
-        if (grow) m = mx;
-      }
-      const float mu = m == -INFINITY ? 0.f : m - 6.f;
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 sl = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
+        const float mu = m == -INFINITY ? 0.f : m - 6.f;
+        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sl = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
 #pragma unroll
-      for (int c = 0; c < BN / 64; ++c) {
-        uint32_t w[32];
+        for (int c = 0; c < BN / 64; ++c) {
+          uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float2 v = make_float2(x[c * 64 + 2 * e], x[c * 64 + 2 * e + 1]);
-          v = fma2(v, sl, nmu);
-          v = make_float2(ex2(v.x), ex2(v.y));
-          sum[e & 1] = add2(sum[e & 1], v);
-          const __half2 hh = __floats2half2_rn(v.x, v.y);
-          w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+          for (int e = 0; e < 32; ++e) {
+            float2 v = make_float2(x[c * 64 + 2 * e], x[c * 64 + 2 * e + 1]);
+            v = fma2(v, sl, nmu);
+            v = make_float2(ex2(v.x), ex2(v.y));
+            sums[e & 1] = add2(sums[e & 1], v);
+            const __half2 hh = __floats2half2_rn(v.x, v.y);
+            w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
+          tmem_st32(s_col + c * 32, w);
         }
-        tmem_st32(s_col + c * 32, w);
+        sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+        if (once) break;
+        again = __any_sync(FULL, sum > 32768.f);
+        if (!again) break;
       }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      if (!ok) break;
+      l += sum;
       tmem_wait_st();
-      // the last block's product: done by now, and a wait on the next phase
-      // would pass at once while this one is open
-      if (n > first &&
-          !(ok = warp_wait_or_quit(&pv_done[tile], (n - 1 - first) & 1, p.wait_limit, &s_quit)))
-        break;
       tc_fence_before();
-      mbar_arrive(&p_full[tile][buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[tile][buf]);
     }
     // ---- O / l ------------------------------------------------------------------------
     if (ok && last > first)
-      ok = warp_wait_or_quit(&pv_done[tile], (last - 1 - first) & 1, p.wait_limit, &s_quit);
+      ok = warp_wait_or_quit(&o_full[tile], 0, p.wait_limit, &s_quit);
     if (ok) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;

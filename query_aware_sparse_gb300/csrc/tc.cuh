@@ -98,24 +98,37 @@ constexpr uint32_t mma_idesc(int m, int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(m >> 4) << 24);
 }
+// One lane of a converged warp. The instructions below take it as a predicate,
+// so that the code around them stays converged and their operands in uniform
+// registers: issued from inside a one-lane branch an MMA cost 65 to 110 cycles
+// of its warp instead of about ten.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p;
+}
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(lead) : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(lead) : "memory");
 }
 // The barrier gets one arrival when every MMA this thread issued so far is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-               :: "r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      :: "r"(smem_u32(bar)), "r"(lead) : "memory");
 }
 
 // ---- barriers and waits -----------------------------------------------------
@@ -124,9 +137,12 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // A wait of one thread: false when `limit` tries (up to about 1 us each) pass,
-// or another role of the CTA has given up; sets the flag then.
+// or another role of the CTA has given up; sets the flag then. The first tries
+// do not sleep.
 __device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, uint32_t limit,
                                              volatile int* quit) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   for (uint32_t i = 0; i < limit; ++i) {
     if (mbar_try_wait_sleep(bar, parity, 1000u)) return true;
     if (*quit) return false;
@@ -137,6 +153,8 @@ __device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, uin
 // The same for a whole warp, which agrees on the outcome.
 __device__ __forceinline__ bool warp_wait_or_quit(uint64_t* bar, uint32_t parity, uint32_t limit,
                                                   volatile int* quit) {
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(FULL, mbar_try_wait(bar, parity))) return true;
   for (uint32_t i = 0; i < limit; ++i) {
     if (__all_sync(FULL, mbar_try_wait_sleep(bar, parity, 1000u))) return true;
     if (__any_sync(FULL, *quit != 0)) return false;
