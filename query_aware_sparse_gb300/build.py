@@ -25,11 +25,11 @@ SOURCES = ["quest_api.cu", "append.cu", "score.cu", "select.cu", "attn.cu", "ste
            "cstep_e4m3_d64.cu", "cstep_e4m3_d128.cu",
            "dense_api.cu", "rope_append.cu", "dense_decode.cu", "prefill.cu",
            "prefill_f16_d64_t1.cu", "prefill_f16_d64_t2.cu", "prefill_f16_d128_t1.cu",
-           "prefill_f16_d128_t2.cu"]
+           "prefill_f16_d128_t2.cu", "prefill_f32.cu"]
 SHARED_HEADERS = ("common.cuh", "internal.h")
 STEP_HEADERS = ("topk.cuh", "attn_dev.cuh", "attn_mma.cuh", "step_impl.cuh", "cstep_impl.cuh")
-DENSE_HEADERS = ("dense.h", "dense.cuh", "dense_rows.cuh", "tc.cuh", "tmap.h",
-                 "prefill_mma.cuh", "dense_decode.cuh", "attn_mma.cuh")
+DENSE_HEADERS = ("dense.h", "dense.cuh", "tc.cuh", "tmap.h",
+                 "prefill_common.cuh", "prefill_mma.cuh", "dense_decode.cuh", "attn_mma.cuh")
 
 
 def headers_of(src):

@@ -1,0 +1,87 @@
+// Prompt attention: what the fp16 and the fp32 kernel share. Rows are cut into
+// blocks of one request's tokens times the group's heads; with few blocks the
+// keys of each are cut into equal parts, whose results are joined at the end.
+#pragma once
+
+#include "dense.cuh"
+#include "tc.cuh"
+
+namespace quest {
+
+struct PrefillArgs {
+  DenseArgs a;
+  int32_t blocks;          // row blocks, an upper bound (sum over requests)
+  int32_t splits;          // equal parts of each block's keys
+  float* part_o;           // [splits, n_q, h_q, D], normalised
+  float* part_lse;         // [splits, n_q, h_q], base 2
+  uint32_t wait_limit;
+};
+
+// Finds row block `idx`, counted over the requests, blocks of `tokens` tokens.
+__device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int idx, int lane,
+                                           int* r_out, int* b_out) {
+  int base = 0;
+  for (int r0 = 0; r0 < a.batch; r0 += 32) {
+    const int r = r0 + lane;
+    const int n = r < a.batch ? a.q_indptr[r + 1] - a.q_indptr[r] : 0;
+    const int cnt = n > 0 ? (n + tokens - 1) / tokens : 0;
+    int incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(FULL, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const int at = idx - base - (incl - cnt);
+    const unsigned hit = __ballot_sync(FULL, at >= 0 && at < cnt);
+    if (hit) {
+      *r_out = r0 + __ffs(hit) - 1;
+      *b_out = __shfl_sync(FULL, at, __ffs(hit) - 1);
+      return true;
+    }
+    base += __shfl_sync(FULL, incl, 31);
+  }
+  return false;
+}
+
+// Joins the splits of each row by log-sum-exp: one warp per (row, query head).
+template <typename O, int D>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) {
+  const DenseArgs& a = p.a;
+  const size_t rows = (size_t)a.q_indptr[a.batch] * a.h_kv * a.group;
+  const size_t all = (size_t)a.n_q * a.h_kv * a.group;
+  const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (at >= rows || at >= all) return;
+  float m = -INFINITY;
+  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[s * all + at]);
+  m = warp_max(m);
+  constexpr int E = D / 32;
+  float o[E] = {}, sum = 0.f;
+  if (m != -INFINITY) {
+    for (int s = 0; s < p.splits; ++s) {
+      const float w = ex2(p.part_lse[s * all + at] - m);
+      sum += w;
+      const float* src = p.part_o + (s * all + at) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  O* dst = static_cast<O*>(a.out) + at * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    if constexpr (sizeof(O) == 2)
+      *reinterpret_cast<__half2*>(dst + e) = __floats2half2_rn(o[e] * inv, o[e + 1] * inv);
+    else
+      *reinterpret_cast<float2*>(dst + e) = make_float2(o[e] * inv, o[e + 1] * inv);
+  }
+  if (lane == 0 && a.lse) a.lse[at] = sum > 0.f ? (m + lg2(sum)) * LN2 : -INFINITY;
+}
+
+template <typename O, int D> cudaError_t launch_prefill_join(const PrefillArgs& p, cudaStream_t s) {
+  const size_t rows = (size_t)p.a.n_q * p.a.h_kv * p.a.group;
+  prefill_join_kernel<O, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace quest

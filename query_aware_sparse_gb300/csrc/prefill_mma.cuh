@@ -30,21 +30,11 @@
 // stale slot would be NaN); such keys' S is replaced, never added to.
 #pragma once
 
-#include "dense.cuh"
-#include "tc.cuh"
+#include "prefill_common.cuh"
 
 namespace quest {
 
 struct PrefillMaps { CUtensorMap q, k, v; };
-
-struct PrefillArgs {
-  DenseArgs a;
-  int32_t blocks;          // row blocks, an upper bound (sum over requests)
-  int32_t splits;          // equal parts of each block's keys
-  float* part_o;           // [splits, n_q, h_q, D], normalised
-  float* part_lse;         // [splits, n_q, h_q], base 2
-  uint32_t wait_limit;
-};
 
 template <int D, int TILES> struct PrefillShape {
   static constexpr int BN = TILES == 2 ? 128 : 64;
@@ -59,39 +49,13 @@ template <int D, int TILES> struct PrefillShape {
   static constexpr int PER_SM = TILES == 2 ? 1 : 2;
 };
 
-// Finds row block `idx`, counted over the requests, blocks of `tokens` tokens.
-__device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int idx, int lane,
-                                           int* r_out, int* b_out) {
-  int base = 0;
-  for (int r0 = 0; r0 < a.batch; r0 += 32) {
-    const int r = r0 + lane;
-    const int n = r < a.batch ? a.q_indptr[r + 1] - a.q_indptr[r] : 0;
-    const int cnt = n > 0 ? (n + tokens - 1) / tokens : 0;
-    int incl = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(FULL, incl, o);
-      if (lane >= o) incl += t;
-    }
-    const int at = idx - base - (incl - cnt);
-    const unsigned hit = __ballot_sync(FULL, at >= 0 && at < cnt);
-    if (hit) {
-      *r_out = r0 + __ffs(hit) - 1;
-      *b_out = __shfl_sync(FULL, at, __ffs(hit) - 1);
-      return true;
-    }
-    base += __shfl_sync(FULL, incl, 31);
-  }
-  return false;
-}
-
 // x -> 2 tanh(y / 2), y = x * to_y, to 3e-7. Two ways that use different
 // pipes: 2 - 4 / (1 + e^y), two values sharing one reciprocal; and y Q(y^2),
 // a polynomial fitted at Chebyshev nodes for |y| < 2 (2.5e-7 off at most). While
 // all of a warp's |y| are below 2 (bit 30 of an fp32 number says so), three
 // pairs of eight take the polynomial: the special function unit alone would
 // take 16 cycles a value, this mix about 9 on either pipe (a 2048-token chunk
-// over 65536 capped keys, 32 heads: 2.95 -> @@ ms). Otherwise every value
+// over 65536 capped keys, 32 heads: 2.95 -> 2.51 ms). Otherwise every value
 // takes the first way by itself.
 template <int N> __device__ __forceinline__ void double_tanh(float (&x)[N], float to_y) {
   uint32_t bits = 0;
@@ -560,36 +524,6 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   if (warp == 4 * TILES + 1) tmem_free(tmem, P::TMEM);
 }
 
-// Joins the splits of each row by log-sum-exp: one warp per (row, query head).
-template <int D>
-__global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) {
-  const DenseArgs& a = p.a;
-  const size_t rows = (size_t)a.q_indptr[a.batch] * a.h_kv * a.group;
-  const size_t all = (size_t)a.n_q * a.h_kv * a.group;
-  const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (at >= rows || at >= all) return;
-  float m = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[s * all + at]);
-  m = warp_max(m);
-  constexpr int E = D / 32;
-  float o[E] = {}, sum = 0.f;
-  if (m != -INFINITY) {
-    for (int s = 0; s < p.splits; ++s) {
-      const float w = ex2(p.part_lse[s * all + at] - m);
-      sum += w;
-      const float* src = p.part_o + (s * all + at) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
-    }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  __half2* dst = reinterpret_cast<__half2*>(static_cast<__half*>(a.out) + at * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = __floats2half2_rn(o[e] * inv, o[e + 1] * inv);
-  if (lane == 0 && a.lse) a.lse[at] = sum > 0.f ? (m + lg2(sum)) * LN2 : -INFINITY;
-}
-
 template <int D, int TILES>
 cudaError_t launch_prefill_mma_t(const PrefillMaps& maps, const PrefillArgs& p, cudaStream_t s) {
   using P = PrefillShape<D, TILES>;
@@ -606,9 +540,7 @@ cudaError_t launch_prefill_mma_t(const PrefillMaps& maps, const PrefillArgs& p, 
                       : (alibi ? go(prefill_mma_kernel<D, TILES, false, true>)
                                : go(prefill_mma_kernel<D, TILES, false, false>));
   if (e != cudaSuccess || p.splits == 1) return e;
-  const size_t rows = (size_t)p.a.n_q * p.a.h_kv * p.a.group;
-  prefill_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_prefill_join<__half, D>(p, s);
 }
 
 }  // namespace quest
