@@ -8,9 +8,10 @@ namespace {
 
 struct Plan { int warps; size_t part_o, part_ml, bytes; };
 
-Plan plan_decode(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim) {
+Plan plan_decode(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim, int32_t dtype) {
   Plan p;
-  p.warps = sm_count() * kDecodeWarps;
+  p.warps = sm_count() * (dtype == QUEST_F16 && head_dim == 64 ? DecodeShape<__half, 64>::WARPS
+                                                               : DecodeShape<float, 64>::WARPS);
   const size_t slots = ((size_t)p.warps + (size_t)batch * h_kv) * group;
   p.part_o = (((size_t)batch + 1) * sizeof(long long) + 255) & ~(size_t)255;
   p.part_ml = p.part_o + slots * head_dim * sizeof(float);
@@ -39,20 +40,33 @@ cudaError_t launch(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) 
   cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel<W, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(dense_decode_kernel<W, D>, p.n_warps / kDecodeWarps, kDecodeWarps * 32, Sh::SMEM, s, maps, p);
+  e = launch_pdl(dense_decode_kernel<W, D>, p.n_warps / Sh::WARPS, Sh::WARPS * 32, Sh::SMEM, s, maps, p);
+  if (e != cudaSuccess) return e;
+  // the same shared memory split as the kernel before it
+  e = cudaFuncSetAttribute(dense_decode_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
   return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, 128, 0, s, p);
+}
+
+template <int D> cudaError_t launch_f32(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) {
+  switch (p.a.group) {
+    case 1: return launch<WarpF32<D, 1>, D>(maps, p, s);
+    case 2: return launch<WarpF32<D, 2>, D>(maps, p, s);
+    case 4: return launch<WarpF32<D, 4>, D>(maps, p, s);
+    default: return launch<WarpF32<D, 8>, D>(maps, p, s);
+  }
 }
 
 }  // namespace
 
 size_t dense_decode_workspace(int32_t batch, int32_t, int32_t h_kv, int32_t group,
-                              int32_t head_dim, int32_t, int32_t) {
-  return plan_decode(batch, h_kv, group, head_dim).bytes;
+                              int32_t head_dim, int32_t, int32_t dtype) {
+  return plan_decode(batch, h_kv, group, head_dim, dtype).bytes;
 }
 
 cudaError_t launch_dense_decode(const DenseArgs& a, cudaStream_t s) {
-  const Plan plan = plan_decode(a.batch, a.h_kv, a.group, a.head_dim);
+  const Plan plan = plan_decode(a.batch, a.h_kv, a.group, a.head_dim, a.dtype);
   char* ws = static_cast<char*>(a.workspace);
   DecodeArgs p{};
   p.a = a;
@@ -67,7 +81,7 @@ cudaError_t launch_dense_decode(const DenseArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   if (a.dtype == QUEST_F16)
     return a.head_dim == 128 ? launch<WarpF16<128>, 128>(maps, p, s) : launch<WarpF16<64>, 64>(maps, p, s);
-  return a.head_dim == 128 ? launch<WarpF32<128>, 128>(maps, p, s) : launch<WarpF32<64>, 64>(maps, p, s);
+  return a.head_dim == 128 ? launch_f32<128>(maps, p, s) : launch_f32<64>(maps, p, s);
 }
 
 }  // namespace quest

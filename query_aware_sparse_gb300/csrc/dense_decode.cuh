@@ -32,8 +32,6 @@ namespace quest {
 
 struct DecodeMaps { CUtensorMap k, v; };
 
-constexpr int kDecodeWarps = 8;
-
 struct DecodeArgs {
   DenseArgs a;
   long long* starts;        // [batch + 1] tiles before each request, all KV heads
@@ -48,8 +46,11 @@ template <typename T, int D> struct DecodeShape {
   static constexpr int COLS = 128 / sizeof(T);               // dims per box
   static constexpr int BOXES = D / COLS;
   static constexpr uint32_t BOX = TT * 128, TILE = BOXES * BOX, STAGE = 2 * TILE;
-  static constexpr int STAGES = 24576 / STAGE;
-  static constexpr uint32_t SMEM = 1024 + kDecodeWarps * STAGES * STAGE;
+  // 192 KB of rings. Half-size tiles (fp16, 64 dims) are bound by their
+  // instructions and take twice the warps.
+  static constexpr int WARPS = sizeof(T) == 2 && D == 64 ? 16 : 8;
+  static constexpr int STAGES = 196608 / WARPS / STAGE;
+  static constexpr uint32_t SMEM = 1024 + WARPS * STAGES * STAGE;
 };
 
 // Tiles per warp: equal runs, of at least four.
@@ -76,13 +77,29 @@ __device__ __forceinline__ Request request_of(const DenseArgs& a, int r, unsigne
   return q;
 }
 
-// Logit -> base 2, with the call's mods.
+// cap tanh(x / cap): for |x| < cap the product of x and a polynomial in
+// (x / cap)^2 (tanh(u) / u fitted at Chebyshev nodes for |u| < 1, 1.1e-7 of
+// itself off at most, so small logits keep their relative accuracy), else tanhf.
+__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
+  const float u = x * inv_cap;
+  if (__any_sync(FULL, !(fabsf(u) < 1.f))) return cap * tanhf(u);
+  const float w = u * u;
+  float q = -0.00042374664917588234f;
+  q = fmaf(q, w, 0.0025196773931384087f);
+  q = fmaf(q, w, -0.008229382336139679f);
+  q = fmaf(q, w, 0.021665599197149277f);
+  q = fmaf(q, w, -0.05393609404563904f);
+  q = fmaf(q, w, 0.13333140313625336f);
+  q = fmaf(q, w, -0.3333333134651184f);
+  return x * fmaf(q, w, 1.f);
+}
+
+// Logit -> base 2, with the call's mods (converged warps only).
 struct Logit {
-  float scale2, cap, slope2;
+  float scale2, cap2, inv_cap2, slope2;
   __device__ __forceinline__ float operator()(float s, int dist) const {
-    float x = s * scale2;
-    if (cap > 0.f) x = cap * LOG2E * tanhf(x / (cap * LOG2E));
-    return x - slope2 * (float)dist;
+    const float x = s * scale2;
+    return (cap2 > 0.f ? capped(x, cap2, inv_cap2) : x) - slope2 * (float)dist;
   }
 };
 
@@ -147,7 +164,8 @@ template <int D> struct WarpF16 {
     const int ta = tok0 + (lane >> 2), tb = ta + 8;
     float x[4];
     if (a.softcap > 0.f || a.slopes) {
-      const Logit f0{scale2, a.softcap, slope2[0]}, f1{scale2, a.softcap, slope2[1]};
+      const float cap2 = a.softcap * LOG2E, inv = 1.f / cap2;
+      const Logit f0{scale2, cap2, inv, slope2[0]}, f1{scale2, cap2, inv, slope2[1]};
       const int da = abs(rq.pos - ta), db = abs(rq.pos - tb);
       x[0] = f0(s0[0] + s1[0], da);
       x[1] = f1(s0[1] + s1[1], da);
@@ -239,22 +257,22 @@ template <int D> struct WarpF16 {
 // The same for fp32 keys. Logits: token lane % 8, chunks lane / 8 + 4 i of
 // four dims (conflict free under the swizzle), q in shared memory; values:
 // D / 32 dims per lane.
-template <int D> struct WarpF32 {
+template <int D, int G> struct WarpF32 {
   using T = float;
-  static constexpr int E = D / 32, G = 8;
+  static constexpr int E = D / 32;
   float m[G], l[G], acc[G][E];
   float slope2[G];
 
   __device__ __forceinline__ void begin(const DenseArgs& a, int r, int g, int lane, float* qs) {
-    const float* q = static_cast<const float*>(a.q) + ((size_t)r * a.h_kv + g) * a.group * D;
+    const float* q = static_cast<const float*>(a.q) + ((size_t)r * a.h_kv + g) * G * D;
     __syncwarp();
-    for (int i = lane; i < a.group * D; i += 32) qs[i] = q[i];
+    for (int i = lane; i < G * D; i += 32) qs[i] = q[i];
     __syncwarp();
 #pragma unroll
     for (int h = 0; h < G; ++h) {
       m[h] = -INFINITY;
       l[h] = 0.f;
-      slope2[h] = a.slopes && h < a.group ? a.slopes[g * a.group + h] * LOG2E : 0.f;
+      slope2[h] = a.slopes ? a.slopes[g * G + h] * LOG2E : 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[h][e] = 0.f;
     }
@@ -272,39 +290,36 @@ template <int D> struct WarpF32 {
       float k[4];
       lds4(k_s + (c >> 3) * 1024 + tok * 128 + (((c & 7) ^ tok) << 4), k);
 #pragma unroll
-      for (int h = 0; h < G; ++h)
-        if (h < a.group) {
-          const float4 q = *reinterpret_cast<const float4*>(qs + h * D + c * 4);
-          s[h] = fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], fmaf(q.w, k[3], s[h]))));
-        }
+      for (int h = 0; h < G; ++h) {
+        const float4 q = *reinterpret_cast<const float4*>(qs + h * D + c * 4);
+        s[h] = fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], fmaf(q.w, k[3], s[h]))));
+      }
     }
     const int at = tok0 + tok, dist = abs(rq.pos - at);
     const bool see = at >= rq.lo && at < rq.hi;
+    const float cap2 = a.softcap * LOG2E, inv_cap2 = 1.f / cap2;
     float p[G];
 #pragma unroll
-    for (int h = 0; h < G; ++h)
-      if (h < a.group) {
-        s[h] += __shfl_xor_sync(FULL, s[h], 8);
-        s[h] += __shfl_xor_sync(FULL, s[h], 16);
-        const Logit f{scale2, a.softcap, slope2[h]};
-        const float x = see ? f(s[h], dist) : -INFINITY;
-        if (__any_sync(FULL, x > m[h] + 8.f)) {
-          float mx = x;
+    for (int h = 0; h < G; ++h) {
+      s[h] += __shfl_xor_sync(FULL, s[h], 8);
+      s[h] += __shfl_xor_sync(FULL, s[h], 16);
+      const Logit f{scale2, cap2, inv_cap2, slope2[h]};
+      const float y = f(s[h], dist), x = see ? y : -INFINITY;
+      if (__any_sync(FULL, x > m[h] + 8.f)) {
+        float mx = x;
 #pragma unroll
-          for (int o = 1; o <= 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-          if (mx > m[h]) {
-            const float w = ex2(m[h] - mx);
-            m[h] = mx;
-            l[h] *= w;
+        for (int o = 1; o <= 4; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        if (mx > m[h]) {
+          const float w = ex2(m[h] - mx);
+          m[h] = mx;
+          l[h] *= w;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[h][e] *= w;
-          }
+          for (int e = 0; e < E; ++e) acc[h][e] *= w;
         }
-        p[h] = ex2(x - (m[h] == -INFINITY ? 0.f : m[h] - 6.f));
-        l[h] += part == 0 ? p[h] : 0.f;
-      } else {
-        p[h] = 0.f;
       }
+      p[h] = ex2(x - (m[h] == -INFINITY ? 0.f : m[h] - 6.f));
+      l[h] += part == 0 ? p[h] : 0.f;
+    }
     const int t0 = max(0, rq.lo - tok0), t1 = min(8, rq.hi - tok0);   // hidden slots are not read
     const int c = lane * E / 4;
     for (int t = t0; t < t1; ++t) {
@@ -313,12 +328,11 @@ template <int D> struct WarpF32 {
       if (E == 4) lds4(addr, v);
       else asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(addr));
 #pragma unroll
-      for (int h = 0; h < G; ++h)
-        if (h < a.group) {
-          const float w = __shfl_sync(FULL, p[h], t);
+      for (int h = 0; h < G; ++h) {
+        const float w = __shfl_sync(FULL, p[h], t);
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e]);
-        }
+        for (int e = 0; e < E; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e]);
+      }
     }
   }
   __device__ __forceinline__ static void lds4(uint32_t addr, float* v) {
@@ -328,30 +342,30 @@ template <int D> struct WarpF32 {
   template <typename F>
   __device__ __forceinline__ void finish(const DenseArgs& a, bool whole, int lane, F put) {
 #pragma unroll
-    for (int h = 0; h < G; ++h)
-      if (h < a.group) {
-        const float sum = warp_sum(l[h]);
-        const float f = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        float* o = put(h, m[h], sum, lane == 0);
+    for (int h = 0; h < G; ++h) {
+      const float sum = warp_sum(l[h]);
+      const float f = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+      float* o = put(h, m[h], sum, lane == 0);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[lane * E + e] = acc[h][e] * f;
-      }
+      for (int e = 0; e < E; ++e) o[lane * E + e] = acc[h][e] * f;
+    }
   }
 };
 
 template <typename W, int D>
-__global__ void __launch_bounds__(kDecodeWarps * 32, 1)
+__global__ void __launch_bounds__(DecodeShape<typename W::T, D>::WARPS * 32, 1)
 dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p) {
   using T = typename W::T;
   using Sh = DecodeShape<T, D>;
-  constexpr int TT = Sh::TT, NST = Sh::STAGES, NW = kDecodeWarps;
+  constexpr int TT = Sh::TT, NST = Sh::STAGES, NW = Sh::WARPS;
   constexpr bool F32 = sizeof(T) == 4;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[NW][NST];
   __shared__ int4 s_meta[NW][NST];
   __shared__ __align__(16) float s_q[F32 ? NW : 1][F32 ? 8 * D : 1];
   const DenseArgs& a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int page_shift = a.page_size == 16 ? 4 : 5;
   const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * NST * Sh::STAGE;
   if (lane < NST) mbar_init(&s_bar[warp][lane], 1);
   fence_mbar_init();
@@ -448,7 +462,7 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
     if (ids_r != r || at < ids_at || at >= ids_at + 32) {
       ids_r = r;
       ids_at = at;
-      ids = at + lane < rq.tiles ? a.page_indices[rq.e0 + (rq.tile0 + at + lane) * TT / a.page_size] : 0;
+      ids = at + lane < rq.tiles ? a.page_indices[rq.e0 + ((rq.tile0 + at + lane) * TT >> page_shift)] : 0;
     }
     const int id = __shfl_sync(FULL, ids, at - ids_at);
     const bool bad = id < 0 || id >= a.n_phys;
@@ -457,7 +471,7 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
       if (!bad) {
         uint64_t* bar = &s_bar[warp][st];
         mbar_expect_tx(bar, Sh::STAGE);
-        const int y = (id * a.h_kv + g) * a.page_size + (rq.tile0 + at) * TT % a.page_size;
+        const int y = ((id * a.h_kv + g) << page_shift) + ((rq.tile0 + at) * TT & (a.page_size - 1));
         const uint32_t dst = ring + st * Sh::STAGE;
 #pragma unroll
         for (int b = 0; b < Sh::BOXES; ++b) {
