@@ -10,11 +10,12 @@
 //
 // Split. A page's summary has one writer: a CTA takes the new tokens of one
 // (request, page) and a run of KV heads with their query heads. It fills a
-// table of cos and sin for its tokens in shared memory once, then each thread
-// takes two 16-byte pieces of one head (the two halves of VEC pairs, or two
-// neighbouring pieces) through all tokens, with the min and max of a key's
-// dims in registers. HBM bound for prompts: every row is read and written
-// once; decode steps are latency bound and spread over the KV heads.
+// table of cos and sin for its tokens in shared memory once, then a warp takes
+// one head at a time: a lane holds two 16-byte pieces (the two halves of VEC
+// pairs, or two neighbouring pieces) of every TG-th token, with the min and max
+// of a key's dims in registers, joined over the token groups by shuffles. HBM
+// bound for prompts: every row is read and written once; decode steps are
+// latency bound and spread over the KV heads.
 #include "common.cuh"
 #include "dense.h"
 
@@ -137,8 +138,16 @@ struct Box {
   }
   __device__ __forceinline__ void fold(uint4 v) {
     const uint4 k = keys(v);
-    mn = make_uint4(K::kmin(mn.x, k.x), K::kmin(mn.y, k.y), K::kmin(mn.z, k.z), K::kmin(mn.w, k.w));
-    mx = make_uint4(K::kmax(mx.x, k.x), K::kmax(mx.y, k.y), K::kmax(mx.z, k.z), K::kmax(mx.w, k.w));
+    join(k, k);
+  }
+  __device__ __forceinline__ static uint4 other(uint4 v, int o) {
+    return make_uint4(__shfl_xor_sync(FULL, v.x, o), __shfl_xor_sync(FULL, v.y, o),
+                      __shfl_xor_sync(FULL, v.z, o), __shfl_xor_sync(FULL, v.w, o));
+  }
+  __device__ __forceinline__ void join(int o) { join(other(mn, o), other(mx, o)); }
+  __device__ __forceinline__ void join(uint4 lo, uint4 hi) {
+    mn = make_uint4(K::kmin(mn.x, lo.x), K::kmin(mn.y, lo.y), K::kmin(mn.z, lo.z), K::kmin(mn.w, lo.w));
+    mx = make_uint4(K::kmax(mx.x, hi.x), K::kmax(mx.y, hi.y), K::kmax(mx.z, hi.z), K::kmax(mx.w, hi.w));
   }
   __device__ __forceinline__ void store(void* lo, void* hi, bool& ovf) const {
     const uint4 a = values(mn), b = values(mx);
@@ -154,32 +163,33 @@ struct Box {
   }
 };
 
-// Two pieces of a row through ntok tokens: the loads of four tokens are in
-// flight before the first is used, then `each` handles them and they are stored.
-template <typename T, typename F>
+// A lane's two pieces of a row, at tokens tg, tg + TG, ...: the loads of four
+// tokens are in flight before the first is used, then `each` handles them and
+// they are stored.
+template <typename T, int TG, typename F>
 __device__ __forceinline__ void walk(const T* src, int64_t src_stride, T* dst, int64_t dst_stride,
-                                     int da, int db, int ntok, F each) {
+                                     int da, int db, int tg, int ntok, F each) {
   constexpr int U = 4;
-  for (int t0 = 0; t0 < ntok; t0 += U) {
+  for (int t0 = tg; t0 < ntok; t0 += U * TG) {
     uint4 x[U], y[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (t0 + u < ntok) {
-        x[u] = ld_v4(src + (t0 + u) * src_stride + da);
-        y[u] = ld_v4(src + (t0 + u) * src_stride + db);
+      if (t0 + u * TG < ntok) {
+        x[u] = ld_v4(src + (t0 + u * TG) * src_stride + da);
+        y[u] = ld_v4(src + (t0 + u * TG) * src_stride + db);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (t0 + u < ntok) {
-        each(x[u], y[u], t0 + u);
-        st_v4(dst + (t0 + u) * dst_stride + da, x[u]);
-        st_v4(dst + (t0 + u) * dst_stride + db, y[u]);
+      if (t0 + u * TG < ntok) {
+        each(x[u], y[u], t0 + u * TG);
+        st_v4(dst + (t0 + u * TG) * dst_stride + da, x[u]);
+        st_v4(dst + (t0 + u * TG) * dst_stride + db, y[u]);
       }
   }
 }
 
 template <typename T, int D, bool F8, bool IL>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppendArgs a) {
   static_assert(!F8 || sizeof(T) == 2, "E4M3 summaries take fp16 keys");
   constexpr int VEC = Elem<T>::kVec;
   constexpr int PC = D / VEC / 2;               // pairs of 16-byte pieces per head
@@ -230,55 +240,66 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeAppendA
   constexpr size_t SE = F8 ? 1 : sizeof(T);     // bytes of a summary element
   bool ovf = false;
 
-  for (int item = threadIdx.x; item < (qn + 2 * nh) * PC; item += kThreads) {
-    const int row = item / PC, it = item % PC;
-    // the item's two pieces, and whether they are rotated
-    int ca = 2 * it, cb = 2 * it + 1;
-    bool turn = ca * VEC < a.rotary_dim;
-    if (!IL) {
-      turn = it * VEC < half;
-      if (turn) { ca = it; cb = it + half / VEC; }
-      // the others, from the rotary part on, in neighbours: 2 * it as above
-    }
-    const float* cs = s_cos + it * VEC;
-    const float* sn = s_sin + it * VEC;
-    auto turned = [&](uint4& x, uint4& y, int tok) {
-      if (turn) rotate<T, IL>(x, y, cs + tok * (D / 2), sn + tok * (D / 2));
-    };
-    ca *= VEC;
-    cb *= VEC;
+  // a warp takes a row at a time: its pieces, at TG tokens side by side
+  constexpr int TG = 32 / PC;
+  const int it = threadIdx.x % PC, tg = threadIdx.x % 32 / PC;
+  // the lane's two pieces, and whether they are rotated
+  int ca = 2 * it, cb = 2 * it + 1;
+  bool turn = ca * VEC < a.rotary_dim;
+  if (!IL) {
+    turn = it * VEC < half;
+    if (turn) { ca = it; cb = it + half / VEC; }
+    // the others, from the rotary part on, in neighbours: 2 * it as above
+  }
+  ca *= VEC;
+  cb *= VEC;
+  const float* cs = s_cos + it * VEC;
+  const float* sn = s_sin + it * VEC;
+  auto turned = [&](uint4& x, uint4& y, int tok) {
+    if (turn) rotate<T, IL>(x, y, cs + tok * (D / 2), sn + tok * (D / 2));
+  };
+  for (int row = threadIdx.x / 32; row < qn + 2 * nh; row += kThreads / 32) {
     if (row < qn) {
       const int h = h0 * a.group + row;
       const int64_t out_stride = (int64_t)a.h_kv * a.group * D;
-      walk(static_cast<const T*>(a.q) + row0 * a.q_stride + h * D, a.q_stride,
-           static_cast<T*>(a.q_out) + row0 * out_stride + h * D, out_stride, ca, cb, ntok, turned);
+      walk<T, TG>(static_cast<const T*>(a.q) + row0 * a.q_stride + h * D, a.q_stride,
+                  static_cast<T*>(a.q_out) + row0 * out_stride + h * D, out_stride, ca, cb, tg, ntok,
+                  turned);
     } else if (pp < 0) {
       break;
     } else if (row < qn + nh) {
       const int h = h0 + row - qn;
       char* sm = static_cast<char*>(a.summary) + (page + h) * 2 * D * SE;
       Box<T, F8> ba, bb;
-      if (fresh) {
+      if (fresh || tg != 0) {
         ba.clear();
         bb.clear();
       } else {
         ba.load(sm + ca * SE, sm + (D + ca) * SE);
         bb.load(sm + cb * SE, sm + (D + cb) * SE);
       }
-      walk(static_cast<const T*>(a.k_new) + row0 * a.k_stride + h * D, a.k_stride,
-           static_cast<T*>(a.k_pool) + ((page + h) * S + slot0) * D, D, ca, cb, ntok,
-           [&](uint4& x, uint4& y, int tok) {
-             turned(x, y, tok);
-             ba.fold(x);
-             bb.fold(y);
-           });
-      ba.store(sm + ca * SE, sm + (D + ca) * SE, ovf);
-      bb.store(sm + cb * SE, sm + (D + cb) * SE, ovf);
+      walk<T, TG>(static_cast<const T*>(a.k_new) + row0 * a.k_stride + h * D, a.k_stride,
+                  static_cast<T*>(a.k_pool) + ((page + h) * S + slot0) * D, D, ca, cb, tg, ntok,
+                  [&](uint4& x, uint4& y, int tok) {
+                    turned(x, y, tok);
+                    ba.fold(x);
+                    bb.fold(y);
+                  });
+      __syncwarp();
+#pragma unroll
+      for (int o = PC; o < 32; o <<= 1) {
+        ba.join(o);
+        bb.join(o);
+      }
+      if (tg == 0) {
+        ba.store(sm + ca * SE, sm + (D + ca) * SE, ovf);
+        bb.store(sm + cb * SE, sm + (D + cb) * SE, ovf);
+      }
     } else {
       const int h = h0 + row - qn - nh;
-      walk(static_cast<const T*>(a.v_new) + row0 * a.v_stride + h * D, a.v_stride,
-           static_cast<T*>(a.v_pool) + ((page + h) * S + slot0) * D, D, ca, cb, ntok,
-           [](uint4&, uint4&, int) {});
+      walk<T, TG>(static_cast<const T*>(a.v_new) + row0 * a.v_stride + h * D, a.v_stride,
+                  static_cast<T*>(a.v_pool) + ((page + h) * S + slot0) * D, D, ca, cb, tg, ntok,
+                  [](uint4&, uint4&, int) {});
     }
   }
   if (F8 && ovf) report(a.err, QUEST_DEVERR_FP8_RANGE);
