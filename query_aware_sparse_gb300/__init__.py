@@ -380,17 +380,23 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, device="cuda"):
     return base ** (-j / rotary_dim)
 
 
-def _expect(name, t, dtype, shape, device, rows=False):
-    """Raises unless t is a dense tensor of this type, shape and device index
-    (with ``rows``, only each row of the first dimension has to be dense)."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on CUDA device {device}, not {t.device}")
-    if not t.is_contiguous():
-        s, d = t.stride(), t.shape[-1]
-        if not rows or t.shape[0] == 1 or s[2] != 1 or s[1] != d or s[0] < t.shape[1] * d:
-            raise ValueError(f"{name} must be contiguous" + (" within its rows" if rows else ""))
+def _expect(name, t, dtype, shape, device):
+    """Raises unless t is a contiguous tensor of this type, shape and CUDA device index."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} on CUDA device {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
+
+
+def _expect_rows(name, t, dtype, shape, device) -> int:
+    """Raises unless t [n, heads, d] has this type, shape and CUDA device index and
+    dense rows, maybe apart; returns the elements from one row to the next."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        n, row, d = shape[0], shape[1] * shape[2], shape[2]
+        s0, s1, s2 = t.stride()
+        if n == 0 or (n == 1 or s0 >= row) and s2 == 1 and (s1 == d or shape[1] == 1):
+            return s0 if n > 1 else row
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)} on CUDA device {device} with contiguous "
+                     f"rows, not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
 
 
 def _current(cache: PagedCache) -> int:
@@ -411,10 +417,6 @@ def _scratch(n, dev, stream):
         return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
 
 
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
 def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_indptr,
                    seq_lens_before, inv_freq, group: int, q_out=None, positions=None,
                    interleaved: bool = False, stream=None):
@@ -425,25 +427,27 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
     positions int32 [n_new] replaces the tokens' places in the cache."""
     dev, dt, n = _current(cache), cache.dtype, k_new.shape[0]
     h, d = cache.h_kv, cache.head_dim
-    _expect("k_new", k_new, dt, (n, h, d), dev, rows=True)
-    _expect("v_new", v_new, dt, (n, h, d), dev, rows=True)
+    kv = (n, h, d)
+    k_stride = _expect_rows("k_new", k_new, dt, kv, dev)
+    v_stride = _expect_rows("v_new", v_new, dt, kv, dev)
     _expect("append_indptr", append_indptr, torch.int32, (table.batch + 1,), dev)
     _expect("seq_lens_before", seq_lens_before, torch.int32, (table.batch,), dev)
     _expect("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
     if positions is not None:
         _expect("positions", positions, torch.int32, (n,), dev)
+    q_stride = 0
     if q is not None:
-        _expect("q", q, dt, (n, h * group, d), dev, rows=True)
+        rows = (n, h * group, d)
+        q_stride = _expect_rows("q", q, dt, rows, dev)
         if q_out is None:
-            q_out = torch.empty((n, h * group, d), dtype=dt, device=dev)
-        _expect("q_out", q_out, dt, (n, h * group, d), dev)
+            q_out = torch.empty(rows, dtype=dt, device=dev)
+        _expect("q_out", q_out, dt, rows, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     rope = QuestRope(_ptr(inv_freq), _ptr(positions), 2 * inv_freq.numel(), int(bool(interleaved)))
     _check(lib().quest_rope_append_kv(
         ctypes.byref(cache.c), ctypes.byref(table.c), ctypes.byref(rope), _ptr(q), _ptr(k_new),
-        _ptr(v_new), 0 if q is None else _row_stride(q), _row_stride(k_new), _row_stride(v_new),
-        int(n), int(group), _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out),
+        _ptr(v_new), q_stride, k_stride, v_stride, n, int(group), _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out),
         _raw_stream(stream, dev)))
     return q_out
 

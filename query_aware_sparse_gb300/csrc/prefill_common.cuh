@@ -12,9 +12,21 @@ struct PrefillArgs {
   DenseArgs a;
   int32_t blocks;          // row blocks, an upper bound (sum over requests)
   int32_t splits;          // equal parts of each block's keys
+  int32_t near_heads;      // KV heads that run side by side
   float* part_o;           // [splits, n_q, h_q, D], normalised
   float* part_lse;         // [splits, n_q, h_q], base 2
   uint32_t wait_limit;
+
+  // CTAs in order: groups of KV heads whose keys stay in L2 while all row
+  // blocks pass (see the plan), row blocks from the last on (the rows that see
+  // most keys first), splits, heads.
+  __device__ __forceinline__ void place(int cta, int h_kv, int* g, int* split, int* idx) const {
+    const int full = blocks * splits * near_heads, group = cta / full;
+    const int heads = min(near_heads, h_kv - group * near_heads), in = cta - group * full;
+    *g = group * near_heads + in % heads;
+    *split = in / heads % splits;
+    *idx = blocks - 1 - in / heads / splits;
+  }
 };
 
 // Finds row block `idx`, counted over the requests, blocks of `tokens` tokens.
@@ -43,27 +55,36 @@ __device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int i
   return false;
 }
 
-// Joins the splits of each row by log-sum-exp: one warp per (row, query head).
+// Joins the splits of each row by log-sum-exp: a warp per (row, query head),
+// its lanes first the splits (weights), then the dims, four splits in flight.
 template <typename O, int D>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) {
   const DenseArgs& a = p.a;
-  const size_t rows = (size_t)a.q_indptr[a.batch] * a.h_kv * a.group;
   const size_t all = (size_t)a.n_q * a.h_kv * a.group;
   const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (at >= rows || at >= all) return;
-  float m = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) m = fmaxf(m, p.part_lse[s * all + at]);
-  m = warp_max(m);
+  if (at >= all || at >= (size_t)a.q_indptr[a.batch] * a.h_kv * a.group) return;
   constexpr int E = D / 32;
-  float o[E] = {}, sum = 0.f;
-  if (m != -INFINITY) {
-    for (int s = 0; s < p.splits; ++s) {
-      const float w = ex2(p.part_lse[s * all + at] - m);
-      sum += w;
-      const float* src = p.part_o + (s * all + at) * D + lane * E;
+  float m = -INFINITY, sum = 0.f, o[E] = {};
+  for (int s0 = 0; s0 < p.splits; s0 += 32) {
+    const float lse = s0 + lane < p.splits ? p.part_lse[(s0 + lane) * all + at] : -INFINITY;
+    const float mx = fmaxf(m, warp_max(lse));
+    if (mx == -INFINITY) continue;
+    const float f = ex2(m - mx), w = ex2(lse - mx);
+    m = mx;
+    sum = sum * f + warp_sum(w);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+    for (int e = 0; e < E; ++e) o[e] *= f;
+    const int n = min(32, p.splits - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float* src = p.part_o + ((s0 + s) * all + at) * D + lane * E;
+      const float ws = __shfl_sync(FULL, w, s);
+      float v[E];
+      if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(ws, v[e], o[e]);
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;

@@ -33,13 +33,11 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
   const int tid = threadIdx.x, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
   const int G = a.group, S = a.page_size, hq = a.h_kv * G, tokens = kRows / G;
 
-  int b = blockIdx.x;
-  const int g = b % a.h_kv;
-  b /= a.h_kv;
-  const int split = b % p.splits;
+  int g, split, idx;
+  p.place(blockIdx.x, a.h_kv, &g, &split, &idx);
   if (tid < 32) {
     int r = -1, blk = 0;
-    const bool found = find_block(a, tokens, p.blocks - 1 - b / p.splits, lane, &r, &blk);
+    const bool found = find_block(a, tokens, idx, lane, &r, &blk);
     if (lane == 0) { s_req = found ? r : -1; s_blk = blk; s_lo = 0x7fffffff; s_hi = 0; }
   }
   __syncthreads();

@@ -34,7 +34,7 @@
 
 namespace quest {
 
-struct PrefillMaps { CUtensorMap q, k, v; };
+struct PrefillMaps { CUtensorMap q, k, v, out; };
 
 template <int D, int TILES> struct PrefillShape {
   static constexpr int BN = TILES == 2 ? 128 : 64;
@@ -104,154 +104,147 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   __shared__ __align__(8) uint64_t q_full, full[STAGES], empty[STAGES], aux, drain;
   __shared__ __align__(8) uint64_t s_full[TILES][SBUF], p_full[TILES][SBUF], pv_done[TILES], o_full[TILES];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_req, s_blk, s_lo[TILES], s_hi[TILES], s_bad;
-  __shared__ volatile int s_quit;
+  __shared__ volatile int s_quit, s_bad;
 
   const DenseArgs& a = p.a;
   const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = a.group, S = a.page_size, hq = a.h_kv * G;
   const int page_shift = S == 16 ? 4 : 5;
-  const int tile_tokens = 128 / G, block_tokens = TILES * tile_tokens;
+  const int tile_tokens = 128 / G;
+  int g, split, idx;
+  p.place(blockIdx.x, a.h_kv, &g, &split, &idx);
 
-  // CTAs in order: KV head, split, then row blocks from the last on (the rows
-  // that see most keys first)
-  int b = blockIdx.x;
-  const int g = b % a.h_kv;
-  b /= a.h_kv;
-  const int split = b % p.splits;
-  const int idx = p.blocks - 1 - b / p.splits;
-
-  if (warp == 0) {
-    int r = -1, blk = 0;
-    const bool found = find_block(a, block_tokens, idx, lane, &r, &blk);
-    if (lane == 0) {
-      s_req = found ? r : -1;
-      s_blk = blk;
-      s_quit = 0;
-      s_bad = 0;
-      for (int t = 0; t < TILES; ++t) { s_lo[t] = 0x7fffffff; s_hi[t] = 0; }
-    }
-  } else if (warp == 1 && lane == 0) {
-    mbar_init(&q_full, 1);
-    mbar_init(&aux, 1);
-    mbar_init(&drain, 1);
-    for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    for (int t = 0; t < TILES; ++t) {
-      for (int i = 0; i < SBUF; ++i) { mbar_init(&s_full[t][i], 1); mbar_init(&p_full[t][i], 4); }
-      mbar_init(&pv_done[t], 1);
-      mbar_init(&o_full[t], 1);
-    }
-    fence_mbar_init();
-  }
-  __syncthreads();
-  const int r = s_req;
-  if (r < 0) return;                                   // past the last row block
-
+  // Every warp finds the row block and its keys by itself: nothing to wait for
+  // until the first copies are on their way.
+  int r = 0, blk = 0;
+  if (!find_block(a, TILES * tile_tokens, idx, lane, &r, &blk)) return;   // past the last one
   const int row0 = a.q_indptr[r], n_r = a.q_indptr[r + 1] - row0;
   const int e0 = a.page_indptr[r], len = a.seq_lens[r];
   const int held = held_tokens(len, a.page_indptr[r + 1] - e0, S, threadIdx.x ? nullptr : a.err);
-  const int tok0 = s_blk * block_tokens;               // first token of the row block
+  const int prefix = a.prefix_lens ? a.prefix_lens[r] : 0;
+  const int tok0 = blk * TILES * tile_tokens;          // first token of the row block
 
-  // what this thread's row sees (softmax warps)
-  const int tile = warp >> 2;                          // of a softmax warp
-  const int tok = tok0 + (TILES == 2 ? tile : 0) * tile_tokens + (threadIdx.x & 127) / G;
-  const int pos = len - n_r + tok;
-  const bool softmax_warp = warp < 4 * TILES;
-  const bool valid = softmax_warp && tok < n_r;
-  Seen seen{0, 0};
-  if (valid) {
-    seen = seen_keys(pos, held, a.window, a.doc_starts ? a.doc_starts[row0 + tok] : 0,
-                     a.prefix_lens ? a.prefix_lens[r] : 0);
-    if (seen.hi <= seen.lo) seen = Seen{0, 0};
+  // key blocks of each tile and of all: from the least that its first row may
+  // see to the most its last may (both grow with the position)
+  int t0[TILES], t1[TILES], n0 = 0x7fffffff, n1 = 0;
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    const int ta = tok0 + t * tile_tokens, tb = min(n_r, ta + tile_tokens);
+    int doc = 0x7fffffff;
+    if (a.doc_starts) {
+      for (int i = ta + lane; i < tb; i += 32) doc = min(doc, a.doc_starts[row0 + i]);
+      doc = __reduce_min_sync(FULL, doc);
+    } else {
+      doc = 0;
+    }
+    const int lo = seen_keys(len - n_r + ta, held, a.window, doc, prefix).lo;
+    const int hi = seen_keys(len - n_r + tb - 1, held, 0, 0, prefix).hi;
+    const bool any = ta < tb && hi > lo;
+    t0[t] = any ? lo / BN : 0;
+    t1[t] = any ? (hi + BN - 1) / BN : 0;
+    if (any) {
+      n0 = min(n0, t0[t]);
+      n1 = max(n1, t1[t]);
+    }
   }
-  if (softmax_warp) {
-    const int lo = __reduce_min_sync(FULL, seen.hi > 0 ? seen.lo : 0x7fffffff);
-    const int hi = __reduce_max_sync(FULL, seen.hi);
-    if (lane == 0 && hi > 0) {
-      atomicMin(&s_lo[tile], lo);
-      atomicMax(&s_hi[tile], hi);
+  if (n1 == 0) n0 = 0;
+  if (p.splits > 1) {
+    const int nb = n1 - n0, first = n0;
+    n0 = first + (int)((long long)nb * split / p.splits);
+    n1 = first + (int)((long long)nb * (split + 1) / p.splits);
+  }
+#pragma unroll
+  for (int t = 0; t < TILES; ++t) {
+    t0[t] = max(n0, t0[t]);
+    t1[t] = min(n1, t1[t]);
+  }
+  const bool softmax_warp = warp < 4 * TILES;
+  const uint32_t q_s = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t ring = q_s + TILES * P::Q_TILE;
+  const int pages_per_block = BN / S;
+
+  // K block n's pages into its place of the ring: the lanes' page ids, then a
+  // box per page and 64 dims
+  auto page_of = [&](int n) {
+    const int lp = n * pages_per_block + lane;
+    int id = -1;
+    if (lane < pages_per_block && n < n1 && lp << page_shift < held) id = a.page_indices[e0 + lp];
+    return id >= 0 && id < a.n_phys ? id : -1;
+  };
+  auto copy = [&](const CUtensorMap* map, int id, uint32_t dst, uint64_t* bar, uint32_t bytes) {
+    if (lane == 0 && bytes) mbar_expect_tx(bar, bytes);
+    __syncwarp();
+    if (id >= 0) {
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+        tma_2d(dst + h * BN * 128 + lane * S * 128, map, h * 64, (id * a.h_kv + g) * S, smem_u32(bar));
+    }
+    __syncwarp();
+  };
+  auto block_bytes = [&](int id) { return __popc(__ballot_sync(FULL, id >= 0)) * S * D * 2u; };
+
+  int id = -1;                                         // the loaders' page of the next block
+  if (warp == 4 * TILES) {
+    if (lane == 0) {
+      mbar_init(&q_full, 1);
+      mbar_init(&aux, 1);
+      mbar_init(&drain, 1);
+      for (int i = 0; i < STAGES; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+      for (int t = 0; t < TILES; ++t) {
+        for (int i = 0; i < SBUF; ++i) { mbar_init(&s_full[t][i], 1); mbar_init(&p_full[t][i], 4); }
+        mbar_init(&pv_done[t], 1);
+        mbar_init(&o_full[t], 1);
+      }
+      fence_mbar_init();
+      s_quit = 0;
+      s_bad = 0;
+      if (n1 > n0) {
+        mbar_expect_tx(&q_full, TILES * P::Q_TILE);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h)
+            tma_3d(q_s + t * P::Q_TILE + h * 128 * 128, &maps.q, h * 64, g * G,
+                   row0 + tok0 + t * tile_tokens, smem_u32(&q_full));
+      }
+    }
+    __syncwarp();
+    if (n1 > n0) {
+      id = page_of(n0);
+      const uint32_t bytes = block_bytes(id);
+      copy(&maps.k, id, ring, &full[0], bytes);
+      if (lane == 0 && !bytes) mbar_arrive(&full[0]);
+      id = page_of(n0 + 1);
     }
   } else if (warp == 4 * TILES + 1) {
     tmem_alloc(smem_u32(&s_tmem), P::TMEM);
+  } else if (warp == 4 * TILES + 2) {
+    id = page_of(n0);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
-  // key blocks: of the row block, of this split, of each tile
-  int u0 = s_lo[0], u1 = s_hi[0];
-  if (TILES == 2) { u0 = min(u0, s_lo[TILES - 1]); u1 = max(u1, s_hi[TILES - 1]); }
-  int n0 = u1 > 0 ? u0 / BN : 0, n1 = (u1 + BN - 1) / BN;
-  if (p.splits > 1) {
-    const int nb = n1 - n0, first = n0;
-    n0 = first + (int)((long long)nb * split / p.splits);
-    n1 = first + (int)((long long)nb * (split + 1) / p.splits);
-  }
-  int t0[TILES], t1[TILES];
-#pragma unroll
-  for (int t = 0; t < TILES; ++t) {
-    t0[t] = s_hi[t] > 0 ? max(n0, s_lo[t] / BN) : n1;
-    t1[t] = s_hi[t] > 0 ? min(n1, (s_hi[t] + BN - 1) / BN) : n1;
-  }
-  // pages outside the pool: reported, and looked for block by block if any
-  for (int pg = n0 * BN / S + threadIdx.x; pg < min(n1 * BN, held + S - 1) / S; pg += P::THREADS) {
-    const int id = a.page_indices[e0 + pg];
-    if (id < 0 || id >= a.n_phys) s_bad = 1;
-  }
-  __syncthreads();
-  const bool any_bad = s_bad != 0;
-  if (any_bad && threadIdx.x == 0) report(a.err, QUEST_DEVERR_PAGE_RANGE);
-
-  const uint32_t q_s = (smem_u32(smem_raw) + 1023) & ~1023u;
-  const uint32_t ring = q_s + TILES * P::Q_TILE;
-  const int pages_per_block = BN / S;
-
   // two tiles: 384 threads of 168 registers, 256 x 208 + 128 x 80 = 63488 of 64512
   if (warp == 4 * TILES || warp == 4 * TILES + 2) {
     // ---- loads: one warp the K blocks and Q, another the V blocks ---------------
     if (TILES == 2) regs_down<80>();
     const int kv = warp == 4 * TILES ? 0 : 1;
-    const CUtensorMap* map = kv ? &maps.v : &maps.k;
-    if (kv == 0 && n1 > n0 && lane == 0) {
-      mbar_expect_tx(&q_full, TILES * P::Q_TILE);
-#pragma unroll
-      for (int t = 0; t < TILES; ++t)
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-          tma_3d(q_s + t * P::Q_TILE + h * 128 * 128, &maps.q, h * 64, g * G,
-                 row0 + tok0 + t * tile_tokens, smem_u32(&q_full));
-    }
-    const int held_pages = (held + S - 1) / S;
     uint32_t aux_phase = 0;
     bool go = true;
-    auto page_of = [&](int n) {
-      const int lp = n * pages_per_block + lane;
-      int id = -1;
-      if (lane < pages_per_block && n < n1 && lp < held_pages) id = a.page_indices[e0 + lp];
-      return id >= 0 && id < a.n_phys ? id : -1;
-    };
-    int id = page_of(n0), seq = kv;                    // block seq of the ring's sequence
-    for (int n = n0; n < n1; ++n, seq += 2) {
+    int seq = 2 - kv;                                  // block seq of the ring's sequence
+    for (int n = n0 + 1 - kv; n < n1; ++n, seq += 2) {
       const int next = page_of(n + 1);
       const unsigned have = __ballot_sync(FULL, id >= 0);
-      const uint32_t bytes = __popc(have) * S * D * 2;
+      const uint32_t bytes = block_bytes(id);
       const bool ragged = held < (n + 1) * BN || __popc(have) < pages_per_block;
-      const int y = id >= 0 ? (id * a.h_kv + g) * S : 0;
       const int stage = seq % STAGES;
       if (seq >= STAGES &&
           !(go = warp_wait_or_quit(&empty[stage], (seq / STAGES & 1) ^ 1, p.wait_limit, &s_quit)))
         break;
       const uint32_t dst = ring + stage * P::BLOCK;
-      uint64_t* bar = kv && ragged ? &aux : &full[stage];
-      if (lane == 0 && bytes) mbar_expect_tx(bar, bytes);
-      __syncwarp();
-      if (id >= 0) {
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-          tma_2d(dst + h * BN * 128 + lane * S * 128, map, h * 64, y, smem_u32(bar));
-      }
-      __syncwarp();
+      copy(kv ? &maps.v : &maps.k, id, dst, kv && ragged ? &aux : &full[stage], bytes);
       if (kv && ragged) {
         // zero what is no valid token, then hand the block over
         if (bytes) {
@@ -362,7 +355,21 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   } else if (softmax_warp) {
     // ---- softmax: one row per thread ------------------------------------------------
     if (TILES == 2) regs_up<208>();
-    const int row = threadIdx.x & 127;
+    const int tile = warp >> 2, row = threadIdx.x & 127;
+    const int tok = tok0 + tile * tile_tokens + row / G, pos = len - n_r + tok;
+    const bool valid = tok < n_r;
+    Seen seen{0, 0};
+    if (valid) seen = seen_keys(pos, held, a.window, a.doc_starts ? a.doc_starts[row0 + tok] : 0, prefix);
+    if (seen.hi <= seen.lo) seen = Seen{0, 0};
+    // pages outside the pool: reported, and looked for block by block if any
+    for (int pg = (n0 * BN >> page_shift) + (int)threadIdx.x; pg < min(n1 * BN, held + S - 1) >> page_shift;
+         pg += TILES * 128) {
+      const int page = a.page_indices[e0 + pg];
+      if (page < 0 || page >= a.n_phys) s_bad = 1;
+    }
+    bar_sync<1, TILES * 128>();
+    const bool any_bad = s_bad != 0;
+    if (any_bad && threadIdx.x == 0) report(a.err, QUEST_DEVERR_PAGE_RANGE);
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
     const int h = g * G + row % G;
     const float log2s = a.scale * LOG2E;
@@ -380,8 +387,8 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       unsigned bad = 0;
       if (any_bad) {
         const int lp = n * pages_per_block + lane;
-        const int id = lane < pages_per_block && lp * S < held ? a.page_indices[e0 + lp] : 0;
-        bad = __ballot_sync(FULL, id < 0 || id >= a.n_phys);
+        const int page = lane < pages_per_block && lp << page_shift < held ? a.page_indices[e0 + lp] : 0;
+        bad = __ballot_sync(FULL, page < 0 || page >= a.n_phys);
       }
       if (!(ok = warp_wait_or_quit(&s_full[tile][buf], s_phase >> buf & 1, p.wait_limit, &s_quit))) break;
       s_phase ^= 1u << buf;
@@ -471,6 +478,10 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[tile][buf]);
     }
+    // A full tile goes through the place of its queries (read by now: the
+    // products are done) to one TMA store; another row by row.
+    const bool whole = p.splits == 1 && last > first && tok0 + (tile + 1) * tile_tokens <= n_r;
+    const uint32_t q_at = q_s + tile * P::Q_TILE;
     // ---- O / l ------------------------------------------------------------------------
     if (ok && last > first)
       ok = warp_wait_or_quit(&o_full[tile], 0, p.wait_limit, &s_quit);
@@ -488,24 +499,32 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
           tmem_wait_ld();
           tmem_loaded(o);
         }
-        if (valid) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = last > first ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-          if (p.splits > 1) {
-            float* dst = p.part_o + part * D + c * 32;
+        for (int e = 0; e < 32; ++e)
+          o[e] = last > first ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+        if (p.splits > 1) {
+          float* dst = p.part_o + part * D + c * 32;
+          if (valid) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) st_v4(dst + e, make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
-          } else {
+            for (int e = 0; e < 32; e += 8) st_v8(dst + e, o + e);
+          }
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const __half2 hh = __floats2half2_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                           :: "r"(q_at + (c >> 1) * 128 * 128 + row * 128 + ((((c & 1) * 4 + e) ^ (row & 7)) << 4)),
+                              "r"(w[4 * e]), "r"(w[4 * e + 1]), "r"(w[4 * e + 2]), "r"(w[4 * e + 3]) : "memory");
+          } else if (valid) {
             __half* dst = static_cast<__half*>(a.out) + at * D + c * 32;
-            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const __half2 hh = __floats2half2_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-              w[e] = *reinterpret_cast<const uint32_t*>(&hh);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) st_v4(dst + 2 * e, make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]));
+            for (int e = 0; e < 16; e += 8) st_v8(dst + 2 * e, w + e);
           }
         }
         __syncwarp();
@@ -513,6 +532,17 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       if (valid) {
         if (p.splits > 1) p.part_lse[part] = lse2;
         else if (a.lse) a.lse[at] = lse2 * LN2;
+      }
+    }
+    if (whole) {                                       // the tile's four warps, also after a wait ran out
+      fence_proxy_async_smem();
+      if (tile == 0) bar_sync<2, 128>();
+      else bar_sync<3, 128>();
+      if (row == 0 && !s_quit) {
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf)
+          tma_store_3d(&maps.out, q_at + hf * 128 * 128, hf * 64, g * G, row0 + tok0 + tile * tile_tokens);
+        tma_store_wait();
       }
     }
   } else if (TILES == 2) {

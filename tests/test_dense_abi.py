@@ -152,14 +152,19 @@ def test_binding_refuses_tensors(q):
     for bad in (x.float(), x[0], x.expand(3, 2, 64)):
         with pytest.raises(ValueError, match="x must be"):
             q._expect("x", bad, torch.float16, (1, 2, 64), dev)
+    with pytest.raises(ValueError, match="x must be"):
+        q._expect("x", x, torch.float16, (1, 2, 64), 5)
     wide = torch.zeros((3, 4, 64), dtype=torch.float16)
-    q._expect("part", wide[:, :2], torch.float16, (3, 2, 64), dev, rows=True)
+    part = wide[:, :2]
+    assert q._expect_rows("part", part, torch.float16, (3, 2, 64), dev) == 256
+    assert q._expect_rows("part", part[:1], torch.float16, (1, 2, 64), dev) == 128
+    assert q._expect_rows("part", wide[:, 3:], torch.float16, (3, 1, 64), dev) == 256
     with pytest.raises(ValueError, match="contiguous"):
-        q._expect("part", wide[:, :2], torch.float16, (3, 2, 64), dev)
-    with pytest.raises(ValueError, match="contiguous"):
-        q._expect("part", wide[:, ::2], torch.float16, (3, 2, 64), dev, rows=True)
-    with pytest.raises(ValueError, match="contiguous"):
-        q._expect("part", wide[:1, :2].expand(3, 2, 64), torch.float16, (3, 2, 64), dev, rows=True)
+        q._expect("part", part, torch.float16, (3, 2, 64), dev)
+    for bad in (wide[:, ::2], wide[:1, :2].expand(3, 2, 64), wide[..., ::2].repeat(1, 1, 2).transpose(1, 2)[:, :2],
+                part.float()):
+        with pytest.raises(ValueError, match="part must be"):
+            q._expect_rows("part", bad, torch.float16, (3, 2, 64), dev)
     m = q.ScoreMods(doc_starts=i32)
     with pytest.raises(ValueError, match="doc_starts"):
         m.check(2, 1, 1, dev)
