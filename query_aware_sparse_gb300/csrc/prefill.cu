@@ -1,6 +1,8 @@
 // Prompt attention: the new tokens of each request over its paged cache. Plan,
 // tensor maps and dispatch; fp16 on the tensor cores (prefill_mma.cuh), fp32 on
 // FMA (prefill_f32.cu).
+#include <math.h>
+
 #include "internal.h"
 #include "prefill_mma.cuh"
 #include "tmap.h"
@@ -23,33 +25,57 @@ struct Plan {
   size_t lse_at, bytes;               // of the partial results in the workspace
 };
 
+// Everything the plan knows: sizes, not the requests' lengths (they are on the
+// device), so it goes by their mean.
 Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
                   int32_t head_dim, int32_t page_size, int32_t dtype) {
   Plan p{1, 0, 1, h_kv, 0, 16};
   if (n_q == 0 || batch == 0) return p;
-  // fp16: two tiles where the requests' rows fill more than one on average
   const bool f16 = dtype == QUEST_F16;
-  if (f16 && (long long)n_q * group > 128LL * batch) p.tiles = 2;
-  const int rows = f16 ? p.tiles * 128 : 64, keys = p.tiles == 2 ? 128 : 64;
-  const int per_sm = p.tiles == 2 ? 1 : 2;             // CTAs an SM holds
+  const long long all_keys = (long long)nnz * page_size;
+  const double keys = (double)all_keys / batch, new_keys = (double)n_q / batch;
+  const double seen = keys > new_keys ? keys - new_keys / 2 : keys / 2;   // by a mean row
+  // fp16: two row tiles per CTA where the rows fill them and the loop is long.
+  // Its loop is 15% faster (16384-token prompt: 1.34 against 1.44 ms), but one
+  // tile per CTA hides its start and end behind a second CTA on the SM (2000
+  // tokens, 8 KV heads of 4: 42 against 49 us; packed requests of up to 7000
+  // tokens: 130 against 172 us).
+  if (f16 && new_keys * group > 128 && seen >= 4096) p.tiles = 2;
+  const int rows = f16 ? p.tiles * 128 : 64, block = p.tiles == 2 ? 128 : 64;
   const int tokens = rows / group;
   const long long blocks = (long long)n_q / tokens + batch;
   p.blocks = (int)(blocks < n_q ? blocks : n_q);
   // Many row blocks read the same keys: as many KV heads at a time as fit half
   // of the L2 (16384 tokens of 32 heads: 1.52 ms with all of them, 1.43 with
   // one by one). Otherwise all heads side by side, longest rows first.
-  const long long head_bytes = (long long)nnz * page_size * head_dim * (f16 ? 4 : 8);
+  const long long head_bytes = all_keys * head_dim * (f16 ? 4 : 8);
   if (p.blocks >= 4LL * batch && head_bytes * h_kv > 64ll << 20)
     p.near_heads = head_bytes > 64ll << 20 ? 1 : (int)((64ll << 20) / head_bytes);
-  // Too few CTAs for the device: cut each one's keys. Ragged requests get
-  // twice the CTAs that run at once, so that the long ones even out.
-  const long long units = (long long)p.blocks * h_kv;
-  const long long want = (long long)sm_count() * per_sm * (batch > 1 ? 2 : 1);
-  const long long key_blocks = ((long long)nnz * page_size / batch + keys - 1) / keys;
-  if (units < want) {
-    long long s = (want + units - 1) / units;
-    if (s > (key_blocks + 1) / 2) s = (key_blocks + 1) / 2;
-    if (s > 1) p.splits = (int)s;
+  // Cut each CTA's keys into `splits` parts where that fills the device better
+  // than it costs: a part's results are written, read and joined (about 7 TB/s
+  // and 4 us), and every wave of CTAs starts and ends (5 us; 2 where two CTAs
+  // share an SM). us of a CTA's key block, measured: two tiles 1.24 for 128
+  // keys, one 0.71 for 64 (two CTAs per SM), fp32 24 (D = 128). A 512-token
+  // chunk of 32768 takes 335 us uncut, 186 in 2, 199 in 4, 223 in 8 parts.
+  const double block_us = f16 ? (p.tiles == 2 ? 1.24 : 0.71) : 24.0 * head_dim / 128;
+  const double start_us = p.tiles == 2 ? 5 : 2;
+  const double slots = (double)sm_count() * (p.tiles == 2 ? 1 : 2);
+  const long long full = ((long long)n_q + tokens - 1) / tokens;
+  const double units = (double)(full > batch ? full : batch) * h_kv;
+  const double mean_us = seen / block * block_us;
+  const bool even = batch == 1 && new_keys * 4 < keys;     // CTAs of about one length
+  const double most_us = even ? mean_us : (batch == 1 ? keys / block * block_us : 2 * mean_us);
+  const double part_us = (double)n_q * h_kv * group * head_dim * 8 / 7e6;
+  double best = 0;
+  for (int s = 1; s <= 128 && s * 2.0 <= keys / block + 1; ++s) {
+    double us = units * mean_us / slots;
+    if (even) us = ceil(units * s / slots) * (mean_us / s + start_us);
+    if (us < most_us / s) us = most_us / s;
+    if (s > 1) us += 4 + part_us * s;
+    if (s == 1 || us < 0.97 * best) {
+      best = us;
+      p.splits = s;
+    }
   }
   if (p.splits > 1) {
     const size_t all = (size_t)p.splits * n_q * h_kv * group;
