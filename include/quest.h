@@ -452,7 +452,7 @@ QUEST_API quest_status quest_rope_append_kv(const quest_cache* cache, const ques
  *                  an earlier one)
  *   prefix_lens  : device int32 [batch], or NULL: keys every query of the
  *                  request sees (a prefix that attends in both directions)
- *   softcap      : finite, 0 = none
+ *   softcap      : 0 = none, else finite and at least 1e-6
  *   window       : keys a query sees at most, its own included; 0 = all
  */
 typedef struct quest_score_mods {

@@ -20,7 +20,8 @@ bool valid_stride(int64_t stride, int64_t row, int32_t dtype) {
 
 quest_status check_mods(const quest_score_mods* m) {
   if (!m) return QUEST_OK;
-  if (!(m->softcap >= 0.f) || isinf(m->softcap) || m->window < 0) return QUEST_ERR_INVALID_ARG;
+  if (!(m->softcap == 0.f || m->softcap >= 1e-6f) || isinf(m->softcap) || m->window < 0)
+    return QUEST_ERR_INVALID_ARG;
   return QUEST_OK;
 }
 

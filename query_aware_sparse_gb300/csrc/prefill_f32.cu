@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
   for (int i = tid; i < kRows * C4; i += 256) {
     const int row = i / C4, c = i % C4, tok = tok0 + row / G;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tok < n_r)
+    if (tok < n_r && row0 + tok < a.n_q)
       v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
                                            ((size_t)(row0 + tok) * hq + g * G + row % G) * D + c * 4);
     *reinterpret_cast<float4*>(s_q + row * LD + c * 4) = v;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
 #pragma unroll
     for (int k = 1; k <= 8; k <<= 1) l[i] += __shfl_xor_sync(FULL, l[i], k);
     const int tok = tok0 + (ty * 4 + i) / G;
-    if (tok >= n_r) continue;
+    if (tok >= n_r || row0 + tok >= a.n_q) continue;
     const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
     const float lse2 = l[i] > 0.f ? m[i] + lg2(l[i]) : -INFINITY;
     const size_t at = ((size_t)row0 + tok) * hq + g * G + (ty * 4 + i) % G;

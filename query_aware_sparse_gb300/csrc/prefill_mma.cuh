@@ -357,7 +357,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     if (TILES == 2) regs_up<208>();
     const int tile = warp >> 2, row = threadIdx.x & 127;
     const int tok = tok0 + tile * tile_tokens + row / G, pos = len - n_r + tok;
-    const bool valid = tok < n_r;
+    const bool valid = tok < n_r && row0 + tok < a.n_q;
     Seen seen{0, 0};
     if (valid) seen = seen_keys(pos, held, a.window, a.doc_starts ? a.doc_starts[row0 + tok] : 0, prefix);
     if (seen.hi <= seen.lo) seen = Seen{0, 0};

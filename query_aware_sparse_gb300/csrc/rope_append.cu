@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppe
   const int t_begin = max(pos0, lp * S), t_end = min(pos0 + n_r, (lp + 1) * S);
   const int row0 = first + (t_begin - pos0);
   const int ntok = min(t_end - t_begin, a.n_new - row0);
+  if (ntok <= 0) return;
   const int half = a.rotary_dim / 2;
 
   // a thread keeps its pair through the tokens: one 64-bit division of the turn

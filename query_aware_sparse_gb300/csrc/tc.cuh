@@ -176,11 +176,17 @@ __device__ __forceinline__ bool warp_wait_or_quit(uint64_t* bar, uint32_t parity
   return false;
 }
 
-// A whole 32-byte sector from one thread (rows written thread by thread).
+// A whole 32-byte sector from one thread (rows written thread by thread); in
+// two pieces where the row is on a 16-byte boundary only.
 __device__ __forceinline__ void st_v8(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-                  "r"(r[7]) : "memory");
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+                    "r"(r[6]), "r"(r[7]) : "memory");
+  } else {
+    st_v4(p, make_uint4(r[0], r[1], r[2], r[3]));
+    st_v4(static_cast<char*>(p) + 16, make_uint4(r[4], r[5], r[6], r[7]));
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -84,7 +84,8 @@ def test_every_call_checks_the_cache(q, over, status):
 
 @pytest.mark.parametrize("mods,status", [
     ((None, None, None, -1.0, 0), INVALID), ((None, None, None, float("nan"), 0), INVALID),
-    ((None, None, None, float("inf"), 0), INVALID), ((None, None, None, 0.0, -4), INVALID)])
+    ((None, None, None, float("inf"), 0), INVALID), ((None, None, None, 1e-7, 0), INVALID),
+    ((None, None, None, 0.0, -4), INVALID)])
 def test_attention_refuses_mods(q, mods, status):
     by, L, c, m = ctypes.byref, q.lib(), _cache(q), q.QuestScoreMods(*mods)
     assert L.quest_dense_decode_attn(by(c), by(_pages(q)), FAKE, 4, by(m), FAKE, FAKE, F, FAKE,

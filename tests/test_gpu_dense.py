@@ -307,6 +307,33 @@ def test_workspace_serves_smaller_calls_after_larger_ones():
     assert qs.device_error() == 0
 
 
+@pytest.mark.parametrize("group,d,rows", [(2, 128, [3, 17, 200]), (4, 64, [1, 17, 300])])
+def test_attention_of_buffers_on_16_byte_boundaries(group, d, rows):
+    """Queries, outputs and workspaces that start 16 bytes into an allocation."""
+    import query_aware_sparse_gb300 as qs
+    lens = [3000, 17, 900]
+    case = _rows_case(94, lens, rows, h_kv=2, group=group, d=d, S=16)
+    hq, n = 2 * group, sum(rows)
+    cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(case["table"])
+
+    def off(shape, dtype):
+        size = int(np.prod(shape))
+        t = torch.zeros(size + 64, dtype=dtype, device="cuda")
+        step = 16 // t.element_size()
+        return t[step:step + size].view(shape)
+    q = off((n, hq, d), F16).copy_(case["q"])
+    args = (3, table.nnz, 2, group, d, 16, F16)
+    out, lse = off((n, hq, d), F16), off((n, hq), torch.float32)
+    qs.prefill_attn(cache, table, q, group, dev_i32(case["q_indptr"]), out=out, lse=lse,
+                    workspace=off((qs.prefill_workspace_size(3, n, *args[1:]),), torch.uint8))
+    check_attention(np_of(out), np_of(lse), _reference(case, case["q"], case["q_indptr"]), HALF16, HALF16, 3000)
+    out, lse = off((3, hq, d), torch.float32), off((3, hq), torch.float32)
+    qs.dense_decode_attn(cache, table, off((3, hq, d), F16).copy_(case["q"][:3]), group, out=out, lse=lse,
+                         workspace=off((qs.dense_decode_workspace_size(*args),), torch.uint8))
+    check_attention(np_of(out), np_of(lse), _reference(case, case["q"][:3], np.arange(4)), 0.0, 0.0, 3000)
+    assert qs.device_error() == 0
+
+
 def test_attention_of_far_pages():
     """Pages whose offset in the pool passes 2^31 elements and 2^32 bytes."""
     import query_aware_sparse_gb300 as qs
