@@ -49,14 +49,15 @@ template <int D, int TILES> struct PrefillShape {
   static constexpr int PER_SM = TILES == 2 ? 1 : 2;
 };
 
-// x -> 2 tanh(y / 2), y = x * to_y, to 3e-7. Two ways that use different
-// pipes: 2 - 4 / (1 + e^y), two values sharing one reciprocal; and y Q(y^2),
-// a polynomial fitted at Chebyshev nodes for |y| < 2 (2.5e-7 off at most). While
-// all of a warp's |y| are below 2 (bit 30 of an fp32 number says so), three
-// pairs of eight take the polynomial: the special function unit alone would
-// take 16 cycles a value, this mix about 9 on either pipe (a 2048-token chunk
-// over 65536 capped keys, 32 heads: 2.95 -> 2.51 ms). Otherwise every value
-// takes the first way by itself.
+// x -> 2 tanh(y / 2), y = x * to_y. Two ways that use different pipes:
+// 2 - 4 / (1 + e^y), two values sharing one reciprocal, to 4e-7; and
+// y (1 + y^2 R(y^2)), fitted at Chebyshev nodes for |y| < 2, to 1.1e-7 of
+// itself. While all of a warp's |y| are below 2 (bit 30 of an fp32 number says
+// so), kPolyPairs pairs of eight take the polynomial. A 2048-token chunk over
+// 65536 capped keys with 32 heads takes 2.38, 2.30, 2.29, 2.28 and 2.60 ms with
+// 0, 3, 4, 6 and 8 of them: six, the more exact of the fast ones. Otherwise
+// every value takes the first way by itself.
+constexpr int kPolyPairs = 6;
 template <int N> __device__ __forceinline__ void double_tanh(float (&x)[N], float to_y) {
   uint32_t bits = 0;
 #pragma unroll
@@ -71,14 +72,15 @@ template <int N> __device__ __forceinline__ void double_tanh(float (&x)[N], floa
     for (int c = 0; c < N; c += 2) {
       const float2 y = make_float2(x[c], x[c + 1]);
       float2 v;
-      if (c / 2 % 8 < 3) {
+      if (c / 2 % 8 < kPolyPairs) {
         const float2 w = mul2(y, y);
-        v = fma2(w, both(2.552621083395934e-07f), both(-6.071357347536832e-06f));
-        v = fma2(v, w, both(7.931843720143661e-05f));
-        v = fma2(v, w, both(-0.0008353933808393776f));
-        v = fma2(v, w, both(0.008328373543918133f));
-        v = fma2(v, w, both(-0.08333214372396469f));
-        v = fma2(v, w, both(0.9999999403953552f));
+        v = fma2(w, both(-2.5863442942863912e-08f), both(6.151556135591818e-07f));
+        v = fma2(v, w, both(-8.036506187636405e-06f));
+        v = fma2(v, w, both(8.463124686386436e-05f));
+        v = fma2(v, w, both(-0.00084275146946311f));
+        v = fma2(v, w, both(0.008333212696015835f));
+        v = fma2(v, w, both(-0.0833333283662796f));
+        v = fma2(v, w, both(1.f));
         v = mul2(v, y);
       } else {
         v = mul2(y, both(LOG2E));
