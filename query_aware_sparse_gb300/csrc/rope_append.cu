@@ -4,7 +4,7 @@
 //
 // Mathematics. Pair j of a head at position p turns by p * inv_freq[j]. Only
 // the fraction of a turn matters, so f = inv_freq / (2 pi) is taken once as a
-// 64-bit fixed-point fraction of a turn; p * f mod 2^64 is an exact integer
+// 64-bit fixed-point fraction of a turn (integer arithmetic); p * f mod 2^64 is an exact integer
 // product, and its high word is the angle to 2^-32 turns, however far p is.
 // cos and sin come from sincospif.
 //
@@ -18,6 +18,7 @@
 // latency bound and spread over the KV heads.
 #include "common.cuh"
 #include "dense.h"
+#include "tmap.h"
 
 namespace quest {
 namespace {
@@ -25,47 +26,72 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxPage = 32;      // tokens per page, at most
 
-// The `seg`-th (request, touched page) of the call, counted in request order;
-// false past the last one. Warp 0 scans the requests 32 at a time.
-__device__ bool touched_page(const RopeAppendArgs& a, int seg, int* r_out, int* j_out) {
-  __shared__ int s_r, s_j;
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int base = 0, r_found = -1, j_found = 0;
-    for (int r0 = 0; r0 < a.batch && r_found < 0; r0 += 32) {
-      const int r = r0 + lane;
-      int pages = 0;
-      if (r < a.batch) {
-        const int n = a.append_indptr[r + 1] - a.append_indptr[r];
-        const int p0 = a.seq_lens_before[r];
-        if (n > 0 && p0 >= 0) pages = (p0 + n - 1) / a.page_size - p0 / a.page_size + 1;
-      }
-      int incl = pages;
+// Pages of request r that the call touches.
+__device__ __forceinline__ int touched(const RopeAppendArgs& a, int r) {
+  if (r >= a.batch) return 0;
+  const int n = a.append_indptr[r + 1] - a.append_indptr[r], p0 = a.seq_lens_before[r];
+  return n > 0 && p0 >= 0 ? (p0 + n - 1) / a.page_size - p0 / a.page_size + 1 : 0;
+}
+__device__ __forceinline__ int warp_running_sum(int v, int lane) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += t;
-      }
-      const int at = seg - base - (incl - pages);
-      const unsigned hit = __ballot_sync(FULL, at >= 0 && at < pages);
-      if (hit) {
-        r_found = r0 + __ffs(hit) - 1;
-        j_found = __shfl_sync(FULL, at, __ffs(hit) - 1);
-      }
-      base += __shfl_sync(FULL, incl, 31);
-    }
-    if (lane == 0) { s_r = r_found; s_j = j_found; }
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(FULL, v, o);
+    if (lane >= o) v += t;
   }
-  __syncthreads();
+  return v;
+}
+
+// The `seg`-th (request, touched page) of the call, counted in request order;
+// false past the last one. Up to 32 requests every warp looks by itself, else
+// the CTA scans 256 at a time.
+__device__ bool touched_page(const RopeAppendArgs& a, int seg, int* r_out, int* j_out) {
+  __shared__ int s_r, s_j, s_sum[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.batch <= 32) {
+    const int pages = touched(a, lane), at = seg - (warp_running_sum(pages, lane) - pages);
+    const unsigned hit = __ballot_sync(FULL, at >= 0 && at < pages);
+    if (!hit) return false;
+    *r_out = __ffs(hit) - 1;
+    *j_out = __shfl_sync(FULL, at, __ffs(hit) - 1);
+    return true;
+  }
+  int base = 0;
+  if (threadIdx.x == 0) s_r = -1;
+  for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+    const int pages = touched(a, r0 + (int)threadIdx.x), incl = warp_running_sum(pages, lane);
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int before = base + incl - pages;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += s_sum[w];
+      base += s_sum[w];
+    }
+    const int at = seg - before;
+    if (at >= 0 && at < pages) { s_r = r0 + (int)threadIdx.x; s_j = at; }
+    __syncthreads();
+    if (s_r >= 0) break;
+  }
   *r_out = s_r;
   *j_out = s_j;
   return s_r >= 0;
 }
 
-// Radians per position -> turns per position as a 64-bit fraction.
+// Radians per position -> turns per position as a 64-bit fraction, modulo one
+// turn: the double's mantissa times 2^64 / (2 pi), shifted by its exponent. In
+// integers: the few fp64 units would take longer than everything else here.
 __device__ __forceinline__ unsigned long long turn_fraction(double inv_freq) {
-  const double t = inv_freq * 0.15915494309189533577;          // 1 / (2 pi)
-  return __double2ull_rd((t - floor(t)) * 18446744073709551616.0);
+  const unsigned long long bits = (unsigned long long)__double_as_longlong(inv_freq);
+  const int e = (int)(bits >> 52 & 0x7ff) - 1023;
+  const unsigned long long m = (bits << 11 | 1ull << 63) & (e > -1023 ? ~0ull : 0ull);
+  const unsigned long long c = 2935890503282001226ull;         // 2^64 / (2 pi)
+  const unsigned long long hi = __umul64hi(m, c), lo = m * c;
+  const int s = 63 - e;                                        // (hi : lo) >> s, the low 64 bits
+  unsigned long long f = 0;
+  if (s >= 64) f = s < 128 ? hi >> (s - 64) : 0ull;
+  else if (s > 0) f = hi << (64 - s) | lo >> s;
+  else if (s > -64) f = lo << -s;
+  return inv_freq < 0 ? 0ull - f : f;
 }
 
 template <typename T> struct Pack;
@@ -206,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppe
   if (ntok <= 0) return;
   const int half = a.rotary_dim / 2;
 
-  // a thread keeps its pair through the tokens: one 64-bit division of the turn
+  // a thread keeps its pair through the tokens
   const int jj = threadIdx.x % half;
   const unsigned long long f = turn_fraction(a.inv_freq[jj]);
   for (int t = threadIdx.x / half; t < ntok && threadIdx.x < kThreads / half * half; t += kThreads / half) {
@@ -317,13 +343,16 @@ cudaError_t launch(const RopeAppendArgs& a, dim3 grid, cudaStream_t s) {
 
 cudaError_t launch_rope_append(const RopeAppendArgs& args, cudaStream_t s) {
   RopeAppendArgs a = args;
+  const int sms = sm_count();
   // a request with n new tokens touches at most ceil(n / S) + 1 pages, each
   // with one token at least
   long long segs = (long long)(a.n_new + a.page_size - 1) / a.page_size + 2LL * a.batch;
   if (segs > a.n_new) segs = a.n_new;
-  // few pages (a decode step): one KV head per CTA; many: all heads
+  // Few pages: the KV heads of one are spread over CTAs until every SM has one;
+  // more CTAs only start more often (200 one-token requests of 8 KV heads: 9.5
+  // us with 152 CTAs wanted, 13.6 with 608; 2048 tokens 11.5 and 19.3).
   a.heads_per_cta = a.h_kv;
-  while (a.heads_per_cta > 1 && segs * ((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta) < 608)
+  while (a.heads_per_cta > 1 && segs * ((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta) < sms)
     a.heads_per_cta = (a.heads_per_cta + 1) / 2;
   const dim3 grid((unsigned)segs, (unsigned)((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta));
   if (a.dtype == QUEST_F16 && a.summary_fp8)
