@@ -551,7 +551,8 @@ QUEST_API int32_t quest_set_trace(void* device_buffer, int32_t max_ctas, int32_t
  * waits on a barrier nothing arrives on. mode 2: in later
  * quest_sparse_decode_attn(_noalloc) and quest_union_decode_attn calls, the
  * first copy slot of warp 0 of the first CTA expects 16 bytes more than its
- * copies bring. Either way that wait runs out: the kernel sets
+ * copies bring; in later quest_dense_decode_attn and (fp16)
+ * quest_prefill_attn calls likewise, and there every wait of that CTA gives up. Either way that wait runs out: the kernel sets
  * QUEST_DEVERR_WAIT_TIMEOUT, issues no further copies, waits (bounded) for
  * those in flight and returns, its outputs unspecified; the device stays
  * usable. wait_limit: tries of every bounded in-kernel wait of those calls

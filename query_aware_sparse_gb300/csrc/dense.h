@@ -37,6 +37,7 @@ struct DenseArgs {
   void* workspace;
   int32_t batch, nnz, n_q, n_phys, h_kv, group, page_size, head_dim, dtype;
   float scale;
+  int32_t test_fault;                         // 2: a copy of the first CTA never completes (tests)
   unsigned* err;
 };
 constexpr int32_t kDecodeMaxBatch = 1 << 19;  // its running sums stay in shared memory

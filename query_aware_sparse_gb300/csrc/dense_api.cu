@@ -46,6 +46,7 @@ quest::DenseArgs dense_args(const quest_cache* cache, const quest_pages* pages, 
   a.group = group; a.page_size = cache->page_size; a.head_dim = cache->head_dim;
   a.dtype = cache->dtype;
   a.scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf((float)cache->head_dim);
+  a.test_fault = quest::test_fault_mode();
   a.err = quest::error_word_ptr();
   return a;
 }

@@ -8,9 +8,9 @@
 // every block: it stays until a row's weights of a block sum to more than 2^15
 // (then m is renewed, O and l rescaled, the block's weights done again). The
 // usual block so needs no maximum at all, and no weight passes fp16's 65504;
-// the factor 2^6 keeps small weights out of fp16's subnormal range. P is rounded to fp16 (half
-// a step, 2^-11 of itself) because the second product takes fp16 operands;
-// S, O, m and l stay in fp32.
+// the factor 2^6 keeps small weights out of fp16's subnormal range. P is
+// rounded to fp16 (half a step, 2^-11 of itself) because the second product
+// takes fp16 operands; S, O, m and l stay in fp32.
 //
 // Bound. 4 D flops per (row, visible key) on tcgen05 against 2 D bytes per key
 // and KV head: tensor bound from a few hundred rows on. The softmax runs one
@@ -20,7 +20,8 @@
 // (256 rows, BN = 128) one tile's softmax runs while the tensor core works on
 // the other. With one (few rows; BN = 64) the next block's S is issued before
 // the softmax of the last, and two CTAs share an SM. Warps 0-3 (and 4-7) are
-// the softmax of a tile, one row per thread; then one warp loads, one issues.
+// the softmax of a tile, one row per thread; then one warp loads Q and K, one
+// issues the products, one loads V, one only frees its registers.
 //   shared memory: Q [TILES][D/64][128 rows][64], then a ring of K and V blocks
 //     [D/64][BN keys][64] in order K V K V, all rows of 128 bytes with the
 //     128-byte swizzle, K and V copied by one TMA box per page and 64 dims;
@@ -28,6 +29,12 @@
 // K and V of a block are used by both tiles before their place is refilled.
 // Rows of V that hold no valid token are zeroed in shared memory (0 * NaN of a
 // stale slot would be NaN); such keys' S is replaced, never added to.
+//
+// Measured (d 128): a 16384-token prompt of 32 heads 1425 us, 1540 TFLOP/s (the
+// GPU at its power cap, 1.6 GHz; cuBLAS sustains 1712); in steady state 2560
+// cycles for two tiles and 128 keys, of which the products take 2048. 2048 of
+// 65536 tokens, 8 KV heads of 4, capped, 2280 us; 16 requests of four tokens over
+// up to 32768, 170 us, 5390 GB/s.
 #pragma once
 
 #include "prefill_common.cuh"
@@ -214,6 +221,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     if (n1 > n0) {
       id = page_of(n0);
       const uint32_t bytes = block_bytes(id);
+      if (a.test_fault == 2 && blockIdx.x == 0 && lane == 0) mbar_expect_more(&full[0], 16);
       copy(&maps.k, id, ring, &full[0], bytes);
       if (lane == 0 && !bytes) mbar_arrive(&full[0]);
       id = page_of(n0 + 1);

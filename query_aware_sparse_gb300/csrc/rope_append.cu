@@ -4,7 +4,7 @@
 //
 // Mathematics. Pair j of a head at position p turns by p * inv_freq[j]. Only
 // the fraction of a turn matters, so f = inv_freq / (2 pi) is taken once as a
-// 64-bit fixed-point fraction of a turn (integer arithmetic); p * f mod 2^64 is an exact integer
+// 64-bit fixed-point fraction of a turn; p * f mod 2^64 is an exact integer
 // product, and its high word is the angle to 2^-32 turns, however far p is.
 // cos and sin come from sincospif.
 //
@@ -16,6 +16,12 @@
 // of a key's dims in registers, joined over the token groups by shuffles. HBM
 // bound for prompts: every row is read and written once; decode steps are
 // latency bound and spread over the KV heads.
+//
+// Measured (fp16, d 128): 131072 tokens of 32 heads, pages of 32, 1012 us, 6430
+// GB/s (95% of the copy rate; 1220 us before the token groups, one thread then
+// taking a piece through all tokens); one token of 16 requests, 8 KV heads of
+// 4, E4M3 summaries, 6.2 us. Two CTAs per SM with four tokens in flight beat
+// three with two (1030 and 1106 us).
 #include "common.cuh"
 #include "dense.h"
 #include "tmap.h"

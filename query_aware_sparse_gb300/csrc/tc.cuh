@@ -145,6 +145,10 @@ __device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
 }
 
 // ---- barriers and waits -----------------------------------------------------
+// Bytes the phase waits for beside those announced with arrivals (tests).
+__device__ __forceinline__ void mbar_expect_more(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
