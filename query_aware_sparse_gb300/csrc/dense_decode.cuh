@@ -459,6 +459,7 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   const int total = (int)(last - first);
   const float scale2 = a.scale * LOG2E;
   const uint64_t pol = evict_first_policy();
+  int issued = 0;
   int ids = 0, ids_at = -1, ids_r = -1;                // page ids of 32 tiles, one per lane
 
   const bool fault = a.test_fault == 2 && blockIdx.x == 0 && warp == 0;
@@ -488,11 +489,20 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
         report(a.err, QUEST_DEVERR_PAGE_RANGE);
       }
     }
-    if (++at == rq.tiles) {
+    if (++issued < total && ++at == rq.tiles) {
       at = 0;
       if (++g == a.h_kv) {
         g = 0;
-        do ++r; while (r < a.batch && (rq = request_of<TT>(a, r, nullptr)).tiles == 0);
+        // the next request with a tile, 32 at a time (there is one: more is to come)
+        for (int r0 = r + 1;; r0 += 32) {
+          const int n = r0 + lane < a.batch ? request_of<TT>(a, r0 + lane, nullptr).tiles : 0;
+          const unsigned some = __ballot_sync(FULL, n > 0);
+          if (some || r0 + 32 >= a.batch) {
+            r = some ? r0 + __ffs(some) - 1 : a.batch - 1;
+            break;
+          }
+        }
+        rq = request_of<TT>(a, r, nullptr);
       }
     }
   };

@@ -35,27 +35,46 @@ struct PrefillArgs {
 // each: 185 -> 168 us).
 __device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int idx, int lane,
                                            int* r_out, int* b_out) {
-  int base = 0;
-  for (int r0 = 0; r0 < a.batch; r0 += 32) {
-    const int r = r0 + lane;
-    const int n = r < a.batch ? a.q_indptr[r + 1] - a.q_indptr[r] : 0;
-    const int cnt = n > 0 ? (n + tokens - 1) / tokens : 0;
-    int before = 0, all = 0;
-    const int from = a.batch <= 32 && r < a.batch ? a.seq_lens[r] - n : 0;
+  auto rows_of = [&](int r) { return r < a.batch ? a.q_indptr[r + 1] - a.q_indptr[r] : 0; };
+  auto blocks_of = [&](int n) { return n > 0 ? (n + tokens - 1) / tokens : 0; };
+  // the lane whose request holds block `at` of its own
+  auto found = [&](int r0, int at, int cnt) {
+    const unsigned hit = __ballot_sync(FULL, at >= 0 && at < cnt);
+    if (!hit) return false;
+    *r_out = r0 + __ffs(hit) - 1;
+    *b_out = __shfl_sync(FULL, cnt - 1 - at, __ffs(hit) - 1);
+    return true;
+  };
+  if (a.batch <= 32) {
+    const int n = rows_of(lane), cnt = blocks_of(n);
+    const int from = lane < a.batch ? a.seq_lens[lane] - n : 0;
+    int before = 0;
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const int ck = __shfl_sync(FULL, cnt, k), fk = __shfl_sync(FULL, from, k);
       before += fk > from || (fk == from && k < lane) ? ck : 0;
-      all += ck;
     }
-    const int at = idx - base - before;
-    const unsigned hit = __ballot_sync(FULL, at >= 0 && at < cnt);
-    if (hit) {
-      *r_out = r0 + __ffs(hit) - 1;
-      *b_out = __shfl_sync(FULL, cnt - 1 - at, __ffs(hit) - 1);
-      return true;
+    return found(0, idx - before, cnt);
+  }
+  int base = 0;
+  for (int r0 = 0; r0 < a.batch; r0 += 128) {          // four loads in flight
+    int cnt[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cnt[k] = blocks_of(rows_of(r0 + 32 * k + lane));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int all = __reduce_add_sync(FULL, cnt[k]);
+      if (idx < base + all) {
+        int incl = cnt[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(FULL, incl, o);
+          if (lane >= o) incl += t;
+        }
+        return found(r0 + 32 * k, idx - base - (incl - cnt[k]), cnt[k]);
+      }
+      base += all;
     }
-    base += all;
   }
   return false;
 }

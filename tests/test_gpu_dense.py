@@ -293,6 +293,105 @@ def test_attention_repeats_bit_for_bit_and_replays():
     assert all(torch.equal(x, y) for x, y in zip(a, c))
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace."""
+    case, cache, table, ws_d, ws_p, new = _setup(95)
+    want, got = new(), [new(), new()]
+    _both(case, cache, table, ws_d, ws_p, want)
+    torch.cuda.synchronize()
+    spaces = [(ws_d, ws_p), (torch.empty_like(ws_d), torch.empty_like(ws_p))]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for s, w, g in zip(streams, spaces, got):
+            _both(case, cache, table, *w, g, stream=s)
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(x, y) for x, y in zip(want, g))
+
+
+def test_requests_that_share_pages():
+    """The same physical pages as the prefix of two requests, and twice in one."""
+    import query_aware_sparse_gb300 as qs
+    case = _rows_case(96, [100, 80, 64], [40, 9, 64], h_kv=2, group=2, d=64, S=16)
+    t = case["table"]
+    t.page_indices[t.page_indptr[1]:t.page_indptr[1] + 4] = t.page_indices[:4]
+    t.page_indices[t.page_indptr[2] + 1] = t.page_indices[t.page_indptr[2]]
+    cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(t)
+    out, lse = qs.prefill_attn(cache, table, case["q"].cuda(), 2, dev_i32(case["q_indptr"]))
+    check_attention(np_of(out), np_of(lse), _reference(case, case["q"], case["q_indptr"]), HALF16, HALF16, 100)
+    out, lse = qs.dense_decode_attn(cache, table, case["q"][:3].cuda().contiguous(), 2)
+    check_attention(np_of(out), np_of(lse), _reference(case, case["q"][:3], np.arange(4)), 0.0, 0.0, 100)
+    assert qs.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_nothing_to_see(dtype):
+    """Requests without a token, and rows that belong to no request."""
+    import query_aware_sparse_gb300 as qs
+    case = random_case(97, [0, 0, 0], h_kv=2, group=2, d=64, S=16, dtype=dtype)
+    cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(case["table"])
+    assert table.nnz == 0
+    q = case["q"].cuda()
+    out, lse = qs.dense_decode_attn(cache, table, q, 2)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    out, lse = qs.prefill_attn(cache, table, q, 2, dev_i32([0, 1, 1, 3]))
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    out, lse = torch.full_like(out, 5), torch.full_like(lse, 5)
+    qs.prefill_attn(cache, table, q, 2, dev_i32([0, 0, 0, 0]), out=out, lse=lse)
+    assert (out == 5).all() and (lse == 5).all() and qs.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_padded_batch(dtype):
+    """A few requests among hundreds of empty ones."""
+    lens = [0] * 700
+    for i, n in ((0, 37), (150, 1), (151, 900), (420, 64), (699, 33)):
+        lens[i] = n
+    _decode(random_case(98, lens, h_kv=2, group=2, d=64, S=16, dtype=dtype))
+    rows = [min(n, 40) for n in lens]
+    _prefill(_rows_case(99, lens, rows, h_kv=1, group=2, d=64, S=16, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_prefill_large_batch(dtype):
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 50, 300).tolist()
+    _prefill(_rows_case(100, lens, [min(n, int(k)) for n, k in zip(lens, rng.integers(0, 9, 300))],
+                        h_kv=1, group=4, d=64, S=16, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_window_of_one_and_many_heads(dtype):
+    """Each row sees itself: out = v, lse = its own logit."""
+    import query_aware_sparse_gb300 as qs
+    case = _rows_case(101, [70, 5], [70, 5], h_kv=40, group=8, d=64, S=32, dtype=dtype)
+    cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(case["table"])
+    out, lse = qs.prefill_attn(cache, table, case["q"].cuda(), 8, dev_i32(case["q_indptr"]),
+                               mods=qs.ScoreMods(window=1))
+    v = case["v_tok"].repeat_interleave(8, dim=1)
+    half = 2.0 ** -11 if dtype == F16 else 2.0 ** -22
+    assert (np.abs(np_of(out).astype(np.float64) - np_of(v)) <= 2 * half * np.abs(np_of(v)) + 1e-7).all()
+    last = case["q"][[69, 74]].cuda()
+    out, lse = qs.dense_decode_attn(cache, table, last, 8, mods=qs.ScoreMods(window=1))
+    assert (np.abs(np_of(out) - np_of(v[[69, 74]]).astype(np.float64)) <= 2.0 ** -20 * np.abs(np_of(v[[69, 74]])) + 1e-7).all()
+
+
+def test_without_lse():
+    """lse may be NULL in the C calls."""
+    import ctypes
+    import query_aware_sparse_gb300 as qs
+    case, cache, table, ws_d, ws_p, new = _setup(102)
+    want, out = new(), new()
+    _both(case, cache, table, ws_d, ws_p, want)
+    by, s = ctypes.byref, torch.cuda.current_stream().cuda_stream
+    L, F = qs.lib(), ctypes.c_float(0.0)
+    assert L.quest_dense_decode_attn(by(cache.c), by(table.c), case["qd"].data_ptr(), 2, None, out[0].data_ptr(), None,
+                                     F, ws_d.data_ptr(), ws_d.numel(), s) == 0
+    assert L.quest_prefill_attn(by(cache.c), by(table.c), case["qp"].data_ptr(), 2, case["ind"].data_ptr(), 220, None,
+                                out[2].data_ptr(), None, F, ws_p.data_ptr(), ws_p.numel(), s) == 0
+    assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2])
+
+
 def test_workspace_serves_smaller_calls_after_larger_ones():
     import query_aware_sparse_gb300 as qs
     case, cache, table, ws_d, ws_p, new = _setup(92)
