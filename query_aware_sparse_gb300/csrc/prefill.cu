@@ -41,7 +41,7 @@ Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t
   // tokens, 8 KV heads of 4: 42 against 49 us; packed requests of up to 7000
   // tokens: 130 against 172 us).
   if (f16 && new_keys * group > 128 && seen >= 4096) p.tiles = 2;
-  const int rows = f16 ? p.tiles * 128 : 64, block = p.tiles == 2 ? 128 : 64;
+  const int rows = p.tiles * 128, block = p.tiles == 2 ? 128 : 64;
   const int tokens = rows / group;
   const long long blocks = (long long)n_q / tokens + batch;
   p.blocks = (int)(blocks < n_q ? blocks : n_q);
@@ -55,11 +55,11 @@ Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t
   // than it costs: a part's results are written, read and joined (about 7 TB/s
   // and 4 us), and every wave of CTAs starts and ends (5 us; 2 where two CTAs
   // share an SM). us of a CTA's key block, measured: two tiles 1.24 for 128
-  // keys, one 0.71 for 64 (two CTAs per SM), fp32 24 (D = 128). A 512-token
+  // keys, one 0.71 for 64 (two CTAs per SM), fp32 14 (D = 128). A 512-token
   // chunk of 32768 takes 335 us uncut, 186 in 2, 199 in 4, 223 in 8 parts.
-  const double block_us = f16 ? (p.tiles == 2 ? 1.24 : 0.71) : 24.0 * head_dim / 128;
+  const double block_us = f16 ? (p.tiles == 2 ? 1.24 : 0.71) : 14.0 * head_dim / 128;
   const double start_us = p.tiles == 2 ? 5 : 2;
-  const double slots = (double)sm_count() * (p.tiles == 2 ? 1 : 2);
+  const double slots = (double)sm_count() * (f16 && p.tiles == 1 ? 2 : 1);
   const long long full = ((long long)n_q + tokens - 1) / tokens;
   const double units = (double)(full > batch ? full : batch) * h_kv;
   const double mean_us = seen / block * block_us;

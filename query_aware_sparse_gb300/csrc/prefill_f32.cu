@@ -1,33 +1,39 @@
 // Prompt attention, fp32 (quest_prefill_attn): the same sums on plain FMA, all
 // of it in fp32.
 //
-// A CTA of 256 threads takes 64 rows (tokens times the group's heads) and 64
-// keys at a time from shared memory; a thread 4 rows x 4 keys of S (its keys
+// A CTA of 256 threads takes 128 rows (tokens times the group's heads) and 64
+// keys at a time from shared memory; a thread 8 rows x 4 keys of S (its keys
 // 16 apart, so that rows padded by 16 bytes are read without bank conflicts),
-// then 4 rows x D / 16 dims of O from P (transposed) and V. FMA bound: 8
-// 16-byte shared loads per 64 FMA for S, 3 per 32 for O. Two CTAs per SM hide
-// the loads of the next block.
+// then 8 rows x D / 16 dims of O from P (transposed) and V. FMA bound, if the
+// tile is this large: 12 16-byte shared loads per 128 FMA for S (with 4 x 4 keys
+// 8 per 64, twice what shared memory delivers; 27 -> 31 TFLOP/s at d 64, 36 at 128), 4 per
+// 64 for O. The next block's K and V come by cp.async meanwhile.
 #include "prefill_common.cuh"
 
 namespace quest {
 namespace {
 
-constexpr int kRows = 64, kKeys = 64;
+constexpr int kRows = 128, kKeys = 64, kR = kRows / 16;   // rows of a CTA and of a thread
 
 template <int D> struct ShapeF32 {
   static constexpr int LD = D + 4, LP = kRows + 4;
-  static constexpr int SMEM = (kRows + 2 * kKeys) * LD * (int)sizeof(float);
+  static constexpr int STAGE = 2 * kKeys * LD;         // floats: K, V
+  static constexpr bool P_OVER_K = LP <= LD;           // P takes K's place once S is there
+  static constexpr int SMEM = (kRows * LD + 2 * STAGE + (P_OVER_K ? 0 : kKeys * LP)) * (int)sizeof(float);
 };
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p) {
+__global__ void __launch_bounds__(256, 1) prefill_f32_kernel(const PrefillArgs p) {
   using Sh = ShapeF32<D>;
   constexpr int LD = Sh::LD, LP = Sh::LP, C4 = D / 4, OC = D / 64;
   extern __shared__ __align__(16) float smem[];
   float* s_q = smem;
-  float* s_k = s_q + kRows * LD;
-  float* s_v = s_k + kKeys * LD;
-  float* s_p = s_k;                                    // [key][row], over K once S is there
+  float* s_kv = s_q + kRows * LD;                      // two stages of K, V
   __shared__ int s_req, s_blk, s_lo, s_hi;
   const DenseArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
@@ -48,11 +54,11 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
   const int held = held_tokens(len, a.page_indptr[r + 1] - e0, S, tid ? nullptr : a.err);
   const int tok0 = s_blk * tokens;
 
-  Seen seen[4];
-  int pos[4];
+  Seen seen[kR];
+  int pos[kR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tok = tok0 + (ty * 4 + i) / G;
+  for (int i = 0; i < kR; ++i) {
+    const int tok = tok0 + (ty * kR + i) / G;
     pos[i] = len - n_r + tok;
     seen[i] = Seen{0, 0};
     if (tok < n_r)
@@ -79,10 +85,10 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
   n1 = first + (int)((long long)nb * (split + 1) / p.splits);
 
   const float log2s = a.scale * LOG2E, cap2 = a.softcap * LOG2E;
-  float slope2[4], m[4], l[4], o[4][OC][4];
+  float slope2[kR], m[kR], l[kR], o[kR][OC][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    slope2[i] = a.slopes ? a.slopes[g * G + (ty * 4 + i) % G] * LOG2E : 0.f;
+  for (int i = 0; i < kR; ++i) {
+    slope2[i] = a.slopes ? a.slopes[g * G + (ty * kR + i) % G] * LOG2E : 0.f;
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -91,25 +97,29 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
       for (int e = 0; e < 4; ++e) o[i][c][e] = 0.f;
   }
 
-  for (int n = n0; n < n1; ++n) {
-    const int kb = n * kKeys;
-    unsigned long long bad = 0;                        // keys of pages outside the pool
-    __syncthreads();
+  // K and V rows of block n into its stage; zeros where there is no token
+  auto fetch = [&](int n) {
+    float* s_k = s_kv + (n & 1) * Sh::STAGE;
+    float* s_v = s_k + kKeys * LD;
 #pragma unroll 4
     for (int i = tid; i < kKeys * C4; i += 256) {
-      const int row = i / C4, c = i % C4, j = kb + row;
-      float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-      if (j < held) {
-        const int id = a.page_indices[e0 + j / S];
-        if (id >= 0 && id < a.n_phys) {
-          const size_t at = (((size_t)id * a.h_kv + g) * S + j % S) * D + c * 4;
-          k = *reinterpret_cast<const float4*>(static_cast<const float*>(a.k_pool) + at);
-          v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.v_pool) + at);
-        }
-      }
-      *reinterpret_cast<float4*>(s_k + row * LD + c * 4) = k;
-      *reinterpret_cast<float4*>(s_v + row * LD + c * 4) = v;
+      const int row = i / C4, c = i % C4, j = n * kKeys + row;
+      const int id = n < n1 && j < held ? a.page_indices[e0 + j / S] : -1;
+      const bool there = id >= 0 && id < a.n_phys;
+      const size_t at = there ? (((size_t)id * a.h_kv + g) * S + j % S) * D + c * 4 : 0;
+      cp_async16(s_k + row * LD + c * 4, static_cast<const float*>(a.k_pool) + at, there);
+      cp_async16(s_v + row * LD + c * 4, static_cast<const float*>(a.v_pool) + at, there);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (n0 < n1) fetch(n0);
+  for (int n = n0; n < n1; ++n) {
+    const int kb = n * kKeys;
+    const float* s_k = s_kv + (n & 1) * Sh::STAGE;
+    const float* s_v = s_k + kKeys * LD;
+    float* s_p = Sh::P_OVER_K ? s_kv + (n & 1) * Sh::STAGE : s_kv + 2 * Sh::STAGE;   // [key][row]
+    fetch(n + 1);
+    unsigned long long bad = 0;                        // keys of pages outside the pool
     for (int q = 0; q < kKeys / S; ++q) {
       if (kb + q * S >= held) break;
       const int id = a.page_indices[e0 + kb / S + q];
@@ -118,30 +128,30 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
         if (tid == 0) report(a.err, QUEST_DEVERR_PAGE_RANGE);
       }
     }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();
 
-    float s[4][4];
+    float s[kR][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
     for (int c = 0; c < C4; ++c) {
-      float4 q[4], k[4];
+      float4 k[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[i] = *reinterpret_cast<const float4*>(s_q + (ty * 4 + i) * LD + c * 4);
-        k[i] = *reinterpret_cast<const float4*>(s_k + (tx + 16 * i) * LD + c * 4);
-      }
+      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(s_k + (tx + 16 * j) * LD + c * 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kR; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(s_q + (ty * kR + i) * LD + c * 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          s[i][j] = fmaf(q[i].x, k[j].x, fmaf(q[i].y, k[j].y, fmaf(q[i].z, k[j].z, fmaf(q[i].w, k[j].w, s[i][j]))));
+          s[i][j] = fmaf(q.x, k[j].x, fmaf(q.y, k[j].y, fmaf(q.z, k[j].z, fmaf(q.w, k[j].w, s[i][j]))));
+      }
     }
-    float pt[4][4];                                    // [key][row]
+    if (Sh::P_OVER_K) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       float mx = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -167,43 +177,47 @@ __global__ void __launch_bounds__(256, 2) prefill_f32_kernel(const PrefillArgs p
       const float base = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float w = ex2(s[i][j] - base);
-        l[i] += w;                                     // this thread's keys only
-        pt[j][i] = w;
+        s[i][j] = ex2(s[i][j] - base);
+        l[i] += s[i][j];                               // this thread's keys only
       }
     }
-    __syncthreads();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<float4*>(s_p + (tx + 16 * j) * LP + ty * 4) = make_float4(pt[j][0], pt[j][1], pt[j][2], pt[j][3]);
+#pragma unroll
+      for (int i = 0; i < kR; i += 4)
+        *reinterpret_cast<float4*>(s_p + (tx + 16 * j) * LP + ty * kR + i) =
+            make_float4(s[i][j], s[i + 1][j], s[i + 2][j], s[i + 3][j]);
     __syncwarp();                                      // a warp reads the rows it wrote
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < kKeys; ++k) {
-      const float4 w = *reinterpret_cast<const float4*>(s_p + k * LP + ty * 4);
-      const float wr[4] = {w.x, w.y, w.z, w.w};
+      float w[kR];
+#pragma unroll
+      for (int i = 0; i < kR; i += 4)
+        *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(s_p + k * LP + ty * kR + i);
 #pragma unroll
       for (int c = 0; c < OC; ++c) {
         const float4 v = *reinterpret_cast<const float4*>(s_v + k * LD + c * 64 + tx * 4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          o[i][c][0] = fmaf(wr[i], v.x, o[i][c][0]);
-          o[i][c][1] = fmaf(wr[i], v.y, o[i][c][1]);
-          o[i][c][2] = fmaf(wr[i], v.z, o[i][c][2]);
-          o[i][c][3] = fmaf(wr[i], v.w, o[i][c][3]);
+        for (int i = 0; i < kR; ++i) {
+          o[i][c][0] = fmaf(w[i], v.x, o[i][c][0]);
+          o[i][c][1] = fmaf(w[i], v.y, o[i][c][1]);
+          o[i][c][2] = fmaf(w[i], v.z, o[i][c][2]);
+          o[i][c][3] = fmaf(w[i], v.w, o[i][c][3]);
         }
       }
     }
+    __syncthreads();                                   // the stage may be filled again
   }
 
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kR; ++i) {
 #pragma unroll
     for (int k = 1; k <= 8; k <<= 1) l[i] += __shfl_xor_sync(FULL, l[i], k);
-    const int tok = tok0 + (ty * 4 + i) / G;
+    const int tok = tok0 + (ty * kR + i) / G;
     if (tok >= n_r || row0 + tok >= a.n_q) continue;
     const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
     const float lse2 = l[i] > 0.f ? m[i] + lg2(l[i]) : -INFINITY;
-    const size_t at = ((size_t)row0 + tok) * hq + g * G + (ty * 4 + i) % G;
+    const size_t at = ((size_t)row0 + tok) * hq + g * G + (ty * kR + i) % G;
     const size_t part = (size_t)split * a.n_q * hq + at;
     float* dst = p.splits > 1 ? p.part_o + part * D : static_cast<float*>(a.out) + at * D;
 #pragma unroll
