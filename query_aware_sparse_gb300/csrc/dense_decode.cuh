@@ -375,35 +375,47 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   fence_mbar_init();
   pdl_wait();
 
-  // tiles of every chunk of 32 requests, then their running sum (the ring's
-  // space, before it is used)
-  long long* sums = reinterpret_cast<long long*>(((uintptr_t)smem_raw + 15) & ~(uintptr_t)15);
+  // Tiles of all requests before the run, and the run. A warp looks at 32
+  // requests at a time: with no more than that by itself, else the sums of all
+  // chunks go through the ring's space, before it is used.
   const int chunks = (a.batch + 31) / 32;
   unsigned* err = blockIdx.x == 0 ? a.err : nullptr;
-  for (int c = warp; c < chunks; c += NW) {
+  auto chunk_tiles = [&](int c, unsigned* e) {         // of the lane's request, all KV heads
     const int r = c * 32 + lane;
-    const int n = r < a.batch ? request_of<TT>(a, r, err).tiles : 0;
-    const int sum = __reduce_add_sync(FULL, n);
-    if (lane == 0) sums[c] = (long long)sum * a.h_kv;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    long long base = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 32) {
-      const long long own = c0 + lane < chunks ? sums[c0 + lane] : 0;
-      long long incl = own;
+    return r < a.batch ? (long long)request_of<TT>(a, r, e).tiles * a.h_kv : 0ll;
+  };
+  auto running = [&](long long v) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl += t;
-      }
-      if (c0 + lane < chunks) sums[c0 + lane] = base + incl - own;
-      base += __shfl_sync(FULL, incl, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(FULL, v, o);
+      if (lane >= o) v += t;
     }
-    if (lane == 0) sums[chunks] = base;
+    return v;
+  };
+  long long* sums = reinterpret_cast<long long*>(((uintptr_t)smem_raw + 15) & ~(uintptr_t)15);
+  long long n = 0, incl = 0, all;                      // of the lane's request of the chunk in hand
+  if (chunks == 1) {
+    n = chunk_tiles(0, err);
+    incl = running(n);
+    all = __shfl_sync(FULL, incl, 31);
+  } else {
+    for (int c = warp; c < chunks; c += NW) {
+      const long long sum = __shfl_sync(FULL, running(chunk_tiles(c, err)), 31);
+      if (lane == 0) sums[c] = sum;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      long long base = 0;
+      for (int c0 = 0; c0 < chunks; c0 += 32) {
+        const long long own = c0 + lane < chunks ? sums[c0 + lane] : 0, up = running(own);
+        if (c0 + lane < chunks) sums[c0 + lane] = base + up - own;
+        base += __shfl_sync(FULL, up, 31);
+      }
+      if (lane == 0) sums[chunks] = base;
+    }
+    __syncthreads();
+    all = sums[chunks];
   }
-  __syncthreads();
-  const long long all = sums[chunks];
   const long long run = run_length(all, p.n_warps);
   // neighbouring runs on different SMs: few tiles spread over the device
   const int wid = warp * gridDim.x + blockIdx.x;
@@ -411,15 +423,11 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
 
   // for the joining kernel: where each request starts (a share per CTA)
   for (int c = blockIdx.x * NW + warp; c < chunks; c += gridDim.x * NW) {
-    const int r = c * 32 + lane;
-    const long long n = r < a.batch ? (long long)request_of<TT>(a, r, nullptr).tiles * a.h_kv : 0;
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(FULL, incl, o);
-      if (lane >= o) incl += t;
+    if (chunks > 1) {
+      n = chunk_tiles(c, nullptr);
+      incl = running(n);
     }
-    if (r < a.batch) p.starts[r] = sums[c] + incl - n;
+    if (c * 32 + lane < a.batch) p.starts[c * 32 + lane] = (chunks > 1 ? sums[c] : 0) + incl - n;
     if (c == chunks - 1 && lane == 0) p.starts[a.batch] = all;
   }
 
@@ -428,31 +436,31 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   Request rq{};
   if (first < last) {
     int c = 0;
-    for (int c0 = 0; c0 < chunks; c0 += 32) {
-      const unsigned le = __ballot_sync(FULL, c0 + lane < chunks && sums[c0 + lane] <= first);
-      if (!le) break;
-      c = c0 + 31 - __clz(le);
+    long long base = 0;
+    if (chunks > 1) {
+      // the last chunk that starts at or before it (chunks without tiles start
+      // where the next one does)
+      for (int c0 = 0; c0 < chunks; c0 += 32) {
+        const unsigned le = __ballot_sync(FULL, c0 + lane < chunks && sums[c0 + lane] <= first);
+        if (!le) break;
+        c = c0 + 31 - __clz(le);
+      }
+      base = sums[c];
+      n = chunk_tiles(c, nullptr);
+      incl = running(n);
     }
-    // requests of the chunk without tiles have the same start: the last one wins
-    r = c * 32 + lane;
-    const long long n = r < a.batch ? (long long)request_of<TT>(a, r, nullptr).tiles * a.h_kv : 0;
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(FULL, incl, o);
-      if (lane >= o) incl += t;
-    }
-    const long long off = first - sums[c];
-    const unsigned hit = __ballot_sync(FULL, off >= incl - n && off < incl);
-    const int src = __ffs(hit) - 1;
+    const long long off = first - base;
+    const int src = __ffs(__ballot_sync(FULL, off >= incl - n && off < incl)) - 1;
     r = c * 32 + src;
     const long long in = off - __shfl_sync(FULL, incl - n, src);
     rq = request_of<TT>(a, r, nullptr);
     g = (int)(in / rq.tiles);
     at = (int)(in - (long long)g * rq.tiles);
   }
-  fence_proxy_async_smem();
-  __syncthreads();                                     // sums are read; the ring may fill
+  if (chunks > 1) {
+    fence_proxy_async_smem();
+    __syncthreads();                                   // sums are read; the ring may fill
+  }
   pdl_launch_dependents();
   if (first >= last) return;
 
