@@ -46,7 +46,7 @@ cudaError_t launch(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) 
   e = cudaFuncSetAttribute(dense_decode_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
                            cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return e;
-  return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, 128, 0, s, p);
+  return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, kJoinThreads, 0, s, p);
 }
 
 template <int D> cudaError_t launch_f32(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) {

@@ -570,13 +570,15 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   flush(meta.z + 1);
 }
 
-// Joins the parts of one (request, query head): the CTA's warps take every
-// fourth part each, then their sums meet in shared memory, in a fixed order.
+// Joins the parts of one (request, query head): the threads take the parts'
+// maxima and sums and leave each part's weight in shared memory, then the warps
+// every eighth part's o (loads without anything to wait for), whose sums meet
+// in shared memory, in a fixed order.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <int D>
-__global__ void __launch_bounds__(128) dense_decode_join_kernel(const DecodeArgs p) {
-  constexpr int E = D / 32;
-  __shared__ float s_o[4][D];
-  __shared__ float s_l[4], s_m[4];
+__global__ void __launch_bounds__(kJoinThreads) dense_decode_join_kernel(const DecodeArgs p) {
+  constexpr int E = D / 32, CHUNK = 1024;
+  __shared__ float s_o[kJoinWarps][D], s_w[CHUNK], s_red[2][kJoinWarps];
   const DenseArgs& a = p.a;
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -591,35 +593,64 @@ __global__ void __launch_bounds__(128) dense_decode_join_kernel(const DecodeArgs
     if (threadIdx.x == 0 && a.lse) a.lse[row] = -INFINITY;
     return;
   }
-  const int w0 = (int)(u0 / run), w1 = (int)((u0 + n - 1) / run);
-  if (w0 == w1) return;                                // written whole
-  float m = -INFINITY;
-  for (int w = w0 + (int)threadIdx.x; w <= w1; w += 128)
-    m = fmaxf(m, p.part_ml[((size_t)w + unit) * a.group + h].x);
-  m = warp_max(m);
-  if (lane == 0) s_m[warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float o[E] = {}, l = 0.f;
-  if (m != -INFINITY) {
-#pragma unroll 4
-    for (int w = w0 + warp; w <= w1; w += 4) {
-      const size_t slot = ((size_t)w + unit) * a.group + h;
-      const float2 ml = p.part_ml[slot];
-      const float f = ex2(ml.x - m);                   // a part without a key: m = -inf, f = 0
-      l = fmaf(f, ml.y, l);
+  const int w0 = (int)(u0 / run), parts = (int)((u0 + n - 1) / run) - w0 + 1;
+  if (parts == 1) return;                              // written whole
+  const size_t slot0 = ((size_t)w0 + unit) * a.group + h;
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  for (int c0 = 0; c0 < parts; c0 += CHUNK) {
+    const int cnt = min(CHUNK, parts - c0);
+    float2 ml[CHUNK / kJoinThreads];
+    float mx = m;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(f, p.part_o[slot * D + lane * E + e], o[e]);
+    for (int k = 0; k < CHUNK / kJoinThreads; ++k) {
+      const int i = k * kJoinThreads + threadIdx.x;
+      ml[k] = i < cnt ? p.part_ml[slot0 + (size_t)(c0 + i) * a.group] : make_float2(-INFINITY, 0.f);
+      mx = fmaxf(mx, ml[k].x);
+    }
+    mx = warp_max(mx);
+    __syncthreads();                                   // the last chunk's weights are used
+    if (lane == 0) s_red[0][warp] = mx;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) mx = fmaxf(mx, s_red[0][w]);
+    if (mx == -INFINITY) continue;                     // parts without a key (whole CTA)
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < CHUNK / kJoinThreads; ++k) {
+      const int i = k * kJoinThreads + threadIdx.x;
+      const float f = ex2(ml[k].x - mx);
+      if (i < cnt) s_w[i] = f;
+      sum = fmaf(f, ml[k].y, sum);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    const float f = ex2(m - mx);
+    m = mx;
+    l *= f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += s_red[1][w];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f;
+    const float* src = p.part_o + (slot0 + (size_t)c0 * a.group) * D + lane * E;
+#pragma unroll 8
+    for (int i = warp; i < cnt; i += kJoinWarps) {
+      const float* q = src + (size_t)i * a.group * D;
+      float v[E];
+      if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(q);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(q);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(s_w[i], v[e], o[e]);
     }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  if (lane == 0) s_l[warp] = l;
   __syncthreads();
-  l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
   if (threadIdx.x < D) {
-    const int i = threadIdx.x;
-    out[i] = l > 0.f ? (s_o[0][i] + s_o[1][i] + s_o[2][i] + s_o[3][i]) / l : 0.f;
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) v += s_o[w][threadIdx.x];
+    out[threadIdx.x] = l > 0.f ? v / l : 0.f;
   }
   if (threadIdx.x == 0 && a.lse) a.lse[row] = l > 0.f ? (m - 6.f + lg2(l)) * LN2 : -INFINITY;
 }
