@@ -402,7 +402,7 @@ def _expect_rows(name, t, dtype, shape, device) -> int:
 def _current(cache: PagedCache) -> int:
     """Index of the current device, which has to hold the cache."""
     dev = cache.k_pool.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"the cache must be on the current CUDA device, not {cache.k_pool.device}")
     return dev
 

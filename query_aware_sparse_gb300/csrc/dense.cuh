@@ -28,4 +28,22 @@ __device__ __forceinline__ int held_tokens(int len, int table_pages, int page_si
   return len;
 }
 
+// cap tanh(x / cap): for |x| < cap the product of x and a polynomial in
+// (x / cap)^2 (tanh(u) / u fitted at Chebyshev nodes for |u| < 1, 1.1e-7 of
+// itself off at most, so small logits keep their relative accuracy), else tanhf. Converged
+// warps only.
+__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
+  const float u = x * inv_cap;
+  if (__any_sync(FULL, !(fabsf(u) < 1.f))) return cap * tanhf(u);
+  const float w = u * u;
+  float q = -0.00042374664917588234f;
+  q = fmaf(q, w, 0.0025196773931384087f);
+  q = fmaf(q, w, -0.008229382336139679f);
+  q = fmaf(q, w, 0.021665599197149277f);
+  q = fmaf(q, w, -0.05393609404563904f);
+  q = fmaf(q, w, 0.13333140313625336f);
+  q = fmaf(q, w, -0.3333333134651184f);
+  return x * fmaf(q, w, 1.f);
+}
+
 }  // namespace quest

@@ -81,23 +81,6 @@ __device__ __forceinline__ Request request_of(const DenseArgs& a, int r, unsigne
   return q;
 }
 
-// cap tanh(x / cap): for |x| < cap the product of x and a polynomial in
-// (x / cap)^2 (tanh(u) / u fitted at Chebyshev nodes for |u| < 1, 1.1e-7 of
-// itself off at most, so small logits keep their relative accuracy), else tanhf.
-__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
-  const float u = x * inv_cap;
-  if (__any_sync(FULL, !(fabsf(u) < 1.f))) return cap * tanhf(u);
-  const float w = u * u;
-  float q = -0.00042374664917588234f;
-  q = fmaf(q, w, 0.0025196773931384087f);
-  q = fmaf(q, w, -0.008229382336139679f);
-  q = fmaf(q, w, 0.021665599197149277f);
-  q = fmaf(q, w, -0.05393609404563904f);
-  q = fmaf(q, w, 0.13333140313625336f);
-  q = fmaf(q, w, -0.3333333134651184f);
-  return x * fmaf(q, w, 1.f);
-}
-
 // Logit -> base 2, with the call's mods (converged warps only).
 struct Logit {
   float scale2, cap2, inv_cap2, slope2;

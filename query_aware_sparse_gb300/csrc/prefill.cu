@@ -26,21 +26,27 @@ struct Plan {
 };
 
 // Everything the plan knows: sizes, not the requests' lengths (they are on the
-// device), so it goes by their mean.
+// device), so it goes by their mean. window: 0, or the keys a row sees at most.
 Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
-                  int32_t head_dim, int32_t page_size, int32_t dtype) {
+                  int32_t head_dim, int32_t page_size, int32_t dtype, int32_t window) {
   Plan p{1, 0, 1, h_kv, 0, 16};
   if (n_q == 0 || batch == 0) return p;
   const bool f16 = dtype == QUEST_F16;
   const long long all_keys = (long long)nnz * page_size;
-  const double keys = (double)all_keys / batch, new_keys = (double)n_q / batch;
-  const double seen = keys > new_keys ? keys - new_keys / 2 : keys / 2;   // by a mean row
+  const double new_keys = (double)n_q / batch;
+  double keys = (double)all_keys / batch;
+  double seen = keys > new_keys ? keys - new_keys / 2 : keys / 2;   // by a mean row
   // fp16: two row tiles per CTA where the rows fill them and the loop is long.
   // Its loop is 15% faster (16384-token prompt: 1.34 against 1.44 ms), but one
   // tile per CTA hides its start and end behind a second CTA on the SM (2000
   // tokens, 8 KV heads of 4: 42 against 49 us; packed requests of up to 7000
   // tokens: 130 against 172 us).
   if (f16 && new_keys * group > 128 && seen >= 4096) p.tiles = 2;
+  if (window > 0) {                                    // of a row block, then
+    const double most = (double)window + p.tiles * 128 / group;
+    if (keys > most) keys = most;
+    if (seen > most) seen = most;
+  }
   const int rows = p.tiles * 128, block = p.tiles == 2 ? 128 : 64;
   const int tokens = rows / group;
   const long long blocks = (long long)n_q / tokens + batch;
@@ -67,7 +73,8 @@ Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t
   const double most_us = even ? mean_us : (batch == 1 ? keys / block * block_us : 2 * mean_us);
   const double part_us = (double)n_q * h_kv * group * head_dim * 8 / 7e6;
   double best = 0;
-  for (int s = 1; s <= 128 && s * 2.0 <= keys / block + 1; ++s) {
+  // (more CTAs than eight rounds of them even nothing out any more)
+  for (int s = 1; s <= 128 && (s == 1 || units * s <= 8 * slots) && s * 2.0 <= keys / block + 1; ++s) {
     double us = units * mean_us / slots;
     if (even) us = ceil(units * s / slots) * (mean_us / s + start_us);
     if (us < most_us / s) us = most_us / s;
@@ -118,11 +125,17 @@ cudaError_t launch_f16(const PrefillArgs& p, int tiles, cudaStream_t s) {
 
 size_t prefill_workspace(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
                          int32_t head_dim, int32_t page_size, int32_t dtype) {
-  return plan_prefill(batch, n_q, nnz, h_kv, group, head_dim, page_size, dtype).bytes;
+  return plan_prefill(batch, n_q, nnz, h_kv, group, head_dim, page_size, dtype, 0).bytes;
 }
 
 cudaError_t launch_prefill(const DenseArgs& a, cudaStream_t s) {
-  const Plan plan = plan_prefill(a.batch, a.n_q, a.nnz, a.h_kv, a.group, a.head_dim, a.page_size, a.dtype);
+  // the workspace is sized without a window: one that would take more is not used
+  Plan plan = plan_prefill(a.batch, a.n_q, a.nnz, a.h_kv, a.group, a.head_dim, a.page_size, a.dtype, 0);
+  if (a.window > 0) {
+    const Plan w = plan_prefill(a.batch, a.n_q, a.nnz, a.h_kv, a.group, a.head_dim, a.page_size, a.dtype,
+                                a.window);
+    if (w.bytes <= plan.bytes) plan = w;
+  }
   const PrefillArgs p = prefill_args(a, plan);
   return a.dtype == QUEST_F16 ? launch_f16(p, plan.tiles, s) : launch_prefill_f32(p, s);
 }

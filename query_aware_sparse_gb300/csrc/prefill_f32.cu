@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(256, 1) prefill_f32_kernel(const PrefillArgs p
   n0 = first + (int)((long long)nb * split / p.splits);
   n1 = first + (int)((long long)nb * (split + 1) / p.splits);
 
-  const float log2s = a.scale * LOG2E, cap2 = a.softcap * LOG2E;
+  const float log2s = a.scale * LOG2E, cap2 = a.softcap * LOG2E, inv_cap2 = 1.f / cap2;
   float slope2[kR], m[kR], l[kR], o[kR][OC][4];
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256, 1) prefill_f32_kernel(const PrefillArgs p
       for (int j = 0; j < 4; ++j) {
         const int key = kb + tx + 16 * j;
         float x = s[i][j] * log2s;
-        if (cap2 > 0.f) x = cap2 * tanhf(x / cap2);
+        if (cap2 > 0.f) x = capped(x, cap2, inv_cap2);
         x -= slope2[i] * fabsf((float)(pos[i] - key));
         if (key < seen[i].lo || key >= seen[i].hi || (bad >> (tx + 16 * j) & 1)) x = -INFINITY;
         s[i][j] = x;
