@@ -19,21 +19,6 @@ Plan plan_decode(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim, i
   return p;
 }
 
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename W, int D>
 cudaError_t launch(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) {
   using Sh = DecodeShape<typename W::T, D>;

@@ -70,11 +70,15 @@ Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t
   const double units = (double)(full > batch ? full : batch) * h_kv;
   const double mean_us = seen / block * block_us;
   const bool even = batch == 1 && new_keys * 4 < keys;     // CTAs of about one length
-  const double most_us = even ? mean_us : (batch == 1 ? keys / block * block_us : 2 * mean_us);
+  // the longest: of one request known, of several taken as three times the mean
+  const double longest = batch == 1 || even ? 1 : batch < 3 ? batch : 3;
+  const double most_us = even ? mean_us : batch == 1 ? keys / block * block_us : longest * mean_us;
   const double part_us = (double)n_q * h_kv * group * head_dim * 8 / 7e6;
   double best = 0;
-  // (more CTAs than eight rounds of them even nothing out any more)
-  for (int s = 1; s <= 128 && (s == 1 || units * s <= 8 * slots) && s * 2.0 <= keys / block + 1; ++s) {
+  // (CTAs of less than 2.8 us only start, and more than eight rounds of them even
+  // nothing out any more)
+  for (int s = 1; s == 1 || (s <= 128 && units * s <= 8 * slots && most_us >= 2.8 * s &&
+                             s <= longest * keys / block + 1); ++s) {
     double us = units * mean_us / slots;
     if (even) us = ceil(units * s / slots) * (mean_us / s + start_us);
     if (us < most_us / s) us = most_us / s;

@@ -79,19 +79,25 @@ __device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int i
   return false;
 }
 
-// Joins the splits of each row by log-sum-exp: a warp per (row, query head),
-// its lanes first the splits (weights), then the dims, four splits in flight.
-template <typename O, int D>
+// Joins the splits of each row by log-sum-exp. Few splits: a warp per (row,
+// query head). Many (of few rows, then): a CTA of eight warps per (row, query
+// head), each warp every eighth split, summed in shared memory in a fixed order.
+constexpr int kJoinWarpSplits = 8;
+template <typename O, int D, bool WIDE>
 __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) {
+  constexpr int E = D / 32, NW = WIDE ? 8 : 1;         // warps of a row
+  __shared__ float s_o[WIDE ? 8 : 1][WIDE ? D : 1], s_sum[8], s_m[8];
   const DenseArgs& a = p.a;
   const size_t all = (size_t)a.n_q * a.h_kv * a.group;
-  const size_t at = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t at = WIDE ? blockIdx.x : (size_t)blockIdx.x * 8 + warp;
   if (at >= all || at >= (size_t)a.q_indptr[a.batch] * a.h_kv * a.group) return;
-  constexpr int E = D / 32;
+  // the row's maximum, then each split's weight in the lanes of its warp
+  const int first = WIDE ? warp : 0;                   // this warp's splits: first, first + NW, ..
   float m = -INFINITY, sum = 0.f, o[E] = {};
-  for (int s0 = 0; s0 < p.splits; s0 += 32) {
-    const float lse = s0 + lane < p.splits ? p.part_lse[(s0 + lane) * all + at] : -INFINITY;
+  for (int s0 = first; s0 < p.splits; s0 += 32 * NW) {
+    const int mine = s0 + lane * NW;
+    const float lse = mine < p.splits ? p.part_lse[mine * all + at] : -INFINITY;
     const float mx = fmaxf(m, warp_max(lse));
     if (mx == -INFINITY) continue;
     const float f = ex2(m - mx), w = ex2(lse - mx);
@@ -99,16 +105,36 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) 
     sum = sum * f + warp_sum(w);
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] *= f;
-    const int n = min(32, p.splits - s0);
+    const int n = min(32, (p.splits - s0 + NW - 1) / NW);
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float* src = p.part_o + ((s0 + s) * all + at) * D + lane * E;
-      const float ws = __shfl_sync(FULL, w, s);
+    for (int k = 0; k < n; ++k) {
+      const float* src = p.part_o + ((size_t)(s0 + k * NW) * all + at) * D + lane * E;
+      const float ws = __shfl_sync(FULL, w, k);
       float v[E];
       if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
       else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(ws, v[e], o[e]);
+    }
+  }
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_m[warp] = m;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, s_m[w]);
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int w = 0; w < 8; ++w) {
+      const float f = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - m);
+      sum = fmaf(f, s_sum[w], sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, s_o[w][lane * E + e], o[e]);
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -125,7 +151,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const PrefillArgs p) 
 
 template <typename O, int D> cudaError_t launch_prefill_join(const PrefillArgs& p, cudaStream_t s) {
   const size_t rows = (size_t)p.a.n_q * p.a.h_kv * p.a.group;
-  prefill_join_kernel<O, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+  if (p.splits > kJoinWarpSplits) prefill_join_kernel<O, D, true><<<(unsigned)rows, 256, 0, s>>>(p);
+  else prefill_join_kernel<O, D, false><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
