@@ -30,8 +30,8 @@ __device__ __forceinline__ int held_tokens(int len, int table_pages, int page_si
 
 // cap tanh(x / cap): for |x| < cap the product of x and a polynomial in
 // (x / cap)^2 (tanh(u) / u fitted at Chebyshev nodes for |u| < 1, 1.1e-7 of
-// itself off at most, so small logits keep their relative accuracy), else tanhf. Converged
-// warps only.
+// itself off at most, so small logits keep their relative accuracy), else
+// tanhf. Converged warps only.
 __device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
   const float u = x * inv_cap;
   if (__any_sync(FULL, !(fabsf(u) < 1.f))) return cap * tanhf(u);

@@ -24,8 +24,8 @@
 // lane per dims for the values.
 //
 // Measured (fp16, d 128): 16 requests of 8192 to 131072 tokens, 8 KV heads of 4,
-// 832 us, 6740 GB/s (99% of the copy rate); 32768 tokens of 32 heads 92 us (86%);
-// fp32, 1000 tokens of one head 10.7 us.
+// 832 us, 6740 GB/s (99% of the copy rate); 32768 tokens of 32 heads 90 us (88%);
+// fp32, 1000 tokens of one head 9.7 us.
 #pragma once
 
 #include "attn_mma.cuh"

@@ -30,11 +30,11 @@
 // Rows of V that hold no valid token are zeroed in shared memory (0 * NaN of a
 // stale slot would be NaN); such keys' S is replaced, never added to.
 //
-// Measured (d 128): a 16384-token prompt of 32 heads 1425 us, 1540 TFLOP/s (the
+// Measured (d 128): a 16384-token prompt of 32 heads 1410 us, 1560 TFLOP/s (the
 // GPU at its power cap, 1.6 GHz; cuBLAS sustains 1712); in steady state 2560
 // cycles for two tiles and 128 keys, of which the products take 2048. 2048 of
-// 65536 tokens, 8 KV heads of 4, capped, 2280 us; 16 requests of four tokens over
-// up to 32768, 170 us, 5390 GB/s.
+// 65536 tokens, 8 KV heads of 4, capped, 2240 us; 16 requests of four tokens over
+// up to 32768, 171 us, 5370 GB/s.
 #pragma once
 
 #include "prefill_common.cuh"
