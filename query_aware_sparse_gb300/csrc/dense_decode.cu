@@ -10,14 +10,17 @@ struct Plan { int warps; size_t part_o, part_ml, bytes; };
 
 Plan plan_decode(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim, int32_t dtype) {
   Plan p;
-  p.warps = sm_count() * (dtype == QUEST_F16 && head_dim == 64 ? DecodeShape<__half, 64>::WARPS
-                                                               : DecodeShape<float, 64>::WARPS);
+  p.warps = sm_count() * (dtype != QUEST_F16 ? DecodeShape<float, 64>::WARPS
+                          : head_dim == 64   ? DecodeShape<__half, 64>::WARPS
+                                             : DecodeShape<__half, 128>::WARPS);
   const size_t slots = ((size_t)p.warps + (size_t)batch * h_kv) * group;
   p.part_o = (((size_t)batch + 1) * sizeof(long long) + 255) & ~(size_t)255;
   p.part_ml = p.part_o + slots * head_dim * sizeof(float);
   p.bytes = p.part_ml + slots * sizeof(float2);
   return p;
 }
+
+static_assert(DecodeShape<float, 64>::WARPS == DecodeShape<float, 128>::WARPS, "one plan for fp32");
 
 template <typename W, int D>
 cudaError_t launch(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) {

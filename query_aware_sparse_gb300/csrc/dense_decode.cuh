@@ -24,7 +24,7 @@
 // lane per dims for the values.
 //
 // Measured (fp16, d 128): 16 requests of 8192 to 131072 tokens, 8 KV heads of 4,
-// 832 us, 6740 GB/s (99% of the copy rate); 32768 tokens of 32 heads 90 us (88%);
+// 819 us, 6840 GB/s (101% of the copy rate); 32768 tokens of 32 heads 90 us (88%);
 // fp32, 1000 tokens of one head 9.7 us.
 #pragma once
 
@@ -50,9 +50,11 @@ template <typename T, int D> struct DecodeShape {
   static constexpr int COLS = 128 / sizeof(T);               // dims per box
   static constexpr int BOXES = D / COLS;
   static constexpr uint32_t BOX = TT * 128, TILE = BOXES * BOX, STAGE = 2 * TILE;
-  // 192 KB of rings. Half-size tiles (fp16, 64 dims) are bound by their
-  // instructions and take twice the warps.
-  static constexpr int WARPS = sizeof(T) == 2 && D == 64 ? 16 : 8;
+  // 192 KB of rings. fp16, 128 dims: 8, 10 and 12 warps take 840, 823 and 819 us
+  // for the ragged batch below. Half-size tiles (64 dims) are bound by their
+  // instructions: 16, 20 and 24 warps take 42.1, 41.7 and 50.4 us for 64 capped
+  // requests of up to 8192 tokens.
+  static constexpr int WARPS = sizeof(T) == 4 ? 8 : D == 64 ? 16 : 12;
   static constexpr int STAGES = 196608 / WARPS / STAGE;
   static constexpr uint32_t SMEM = 1024 + WARPS * STAGES * STAGE;
 };
