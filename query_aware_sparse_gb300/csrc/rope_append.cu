@@ -29,7 +29,6 @@
 namespace quest {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxPage = 32;      // tokens per page, at most
 
 // Pages of request r that the call touches.
@@ -49,9 +48,10 @@ __device__ __forceinline__ int warp_running_sum(int v, int lane) {
 
 // The `seg`-th (request, touched page) of the call, counted in request order;
 // false past the last one. Up to 32 requests every warp looks by itself, else
-// the CTA scans 256 at a time.
+// the CTA scans as many as it has threads at a time.
+template <int NT>
 __device__ bool touched_page(const RopeAppendArgs& a, int seg, int* r_out, int* j_out) {
-  __shared__ int s_r, s_j, s_sum[kThreads / 32];
+  __shared__ int s_r, s_j, s_sum[NT / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (a.batch <= 32) {
     const int pages = touched(a, lane), at = seg - (warp_running_sum(pages, lane) - pages);
@@ -63,13 +63,13 @@ __device__ bool touched_page(const RopeAppendArgs& a, int seg, int* r_out, int* 
   }
   int base = 0;
   if (threadIdx.x == 0) s_r = -1;
-  for (int r0 = 0; r0 < a.batch; r0 += kThreads) {
+  for (int r0 = 0; r0 < a.batch; r0 += NT) {
     const int pages = touched(a, r0 + (int)threadIdx.x), incl = warp_running_sum(pages, lane);
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
     int before = base + incl - pages;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
       if (w < warp) before += s_sum[w];
       base += s_sum[w];
     }
@@ -220,15 +220,15 @@ __device__ __forceinline__ void walk(const T* src, int64_t src_stride, T* dst, i
   }
 }
 
-template <typename T, int D, bool F8, bool IL>
-__global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppendArgs a) {
+template <typename T, int D, bool F8, bool IL, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) rope_append_kernel(const RopeAppendArgs a) {
   static_assert(!F8 || sizeof(T) == 2, "E4M3 summaries take fp16 keys");
   constexpr int VEC = Elem<T>::kVec;
   constexpr int PC = D / VEC / 2;               // pairs of 16-byte pieces per head
   __shared__ __align__(16) float s_cos[kMaxPage * D / 2], s_sin[kMaxPage * D / 2];
 
   int r, j;
-  if (!touched_page(a, blockIdx.x, &r, &j)) return;
+  if (!touched_page<NT>(a, blockIdx.x, &r, &j)) return;
   const int S = a.page_size, first = a.append_indptr[r], pos0 = a.seq_lens_before[r];
   const int n_r = a.append_indptr[r + 1] - first;
   const int lp = pos0 / S + j;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppe
   // a thread keeps its pair through the tokens
   const int jj = threadIdx.x % half;
   const unsigned long long f = turn_fraction(a.inv_freq[jj]);
-  for (int t = threadIdx.x / half; t < ntok && threadIdx.x < kThreads / half * half; t += kThreads / half) {
+  for (int t = threadIdx.x / half; t < ntok && threadIdx.x < NT / half * half; t += NT / half) {
     const int p = a.positions ? a.positions[row0 + t] : t_begin + t;
     const int turn = (int)(((unsigned long long)(long long)p * f) >> 32);   // half turns in 2^-31
     float sn, cs;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppe
   auto turned = [&](uint4& x, uint4& y, int tok) {
     if (turn) rotate<T, IL>(x, y, cs + tok * (D / 2), sn + tok * (D / 2));
   };
-  for (int row = threadIdx.x / 32; row < qn + 2 * nh; row += kThreads / 32) {
+  for (int row = threadIdx.x / 32; row < qn + 2 * nh; row += NT / 32) {
     if (row < qn) {
       const int h = h0 * a.group + row;
       const int64_t out_stride = (int64_t)a.h_kv * a.group * D;
@@ -338,11 +338,22 @@ __global__ void __launch_bounds__(kThreads, 2) rope_append_kernel(const RopeAppe
   if (F8 && ovf) report(a.err, QUEST_DEVERR_FP8_RANGE);
 }
 
-template <typename T, int D, bool F8>
-cudaError_t launch(const RopeAppendArgs& a, dim3 grid, cudaStream_t s) {
-  if (a.interleaved) rope_append_kernel<T, D, F8, true><<<grid, kThreads, 0, s>>>(a);
-  else rope_append_kernel<T, D, F8, false><<<grid, kThreads, 0, s>>>(a);
+template <typename T, int D, bool F8, int NT>
+cudaError_t launch_n(const RopeAppendArgs& a, dim3 grid, cudaStream_t s) {
+  if (a.interleaved) rope_append_kernel<T, D, F8, true, NT><<<grid, NT, 0, s>>>(a);
+  else rope_append_kernel<T, D, F8, false, NT><<<grid, NT, 0, s>>>(a);
   return cudaGetLastError();
+}
+
+// Many CTAs of few rows: four warps each, so that more of them start at once
+// (53823 tokens, one KV head of 8, E4M3: 103 us with eight warps, 76 with four;
+// 65536 tokens of one head 61 and 37). From 24 rows on the two are alike, and
+// where the device is not full eight warps get through a page sooner.
+template <typename T, int D, bool F8>
+cudaError_t launch(const RopeAppendArgs& a, dim3 grid, int sms, cudaStream_t s) {
+  const int rows = a.heads_per_cta * ((a.q ? a.group : 0) + 2);
+  const bool small = rows <= 16 && (long long)grid.x * grid.y > 4LL * sms;
+  return small ? launch_n<T, D, F8, 128>(a, grid, s) : launch_n<T, D, F8, 256>(a, grid, s);
 }
 
 }  // namespace
@@ -362,10 +373,10 @@ cudaError_t launch_rope_append(const RopeAppendArgs& args, cudaStream_t s) {
     a.heads_per_cta = (a.heads_per_cta + 1) / 2;
   const dim3 grid((unsigned)segs, (unsigned)((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta));
   if (a.dtype == QUEST_F16 && a.summary_fp8)
-    return a.head_dim == 128 ? launch<__half, 128, true>(a, grid, s) : launch<__half, 64, true>(a, grid, s);
+    return a.head_dim == 128 ? launch<__half, 128, true>(a, grid, sms, s) : launch<__half, 64, true>(a, grid, sms, s);
   if (a.dtype == QUEST_F16)
-    return a.head_dim == 128 ? launch<__half, 128, false>(a, grid, s) : launch<__half, 64, false>(a, grid, s);
-  return a.head_dim == 128 ? launch<float, 128, false>(a, grid, s) : launch<float, 64, false>(a, grid, s);
+    return a.head_dim == 128 ? launch<__half, 128, false>(a, grid, sms, s) : launch<__half, 64, false>(a, grid, sms, s);
+  return a.head_dim == 128 ? launch<float, 128, false>(a, grid, sms, s) : launch<float, 64, false>(a, grid, sms, s);
 }
 
 }  // namespace quest
