@@ -191,6 +191,38 @@ def test_prefill_long_prompt(group, d):
     _prefill(_rows_case(44, [n + 600, 37], [n, 37], h_kv=1, group=group, d=d, S=16))
 
 
+@pytest.mark.parametrize("rows,window", [(520, 0), (2100, 0), (520, 4500)])
+def test_prefill_of_a_cache_beyond_l2_share(rows, window):
+    """Keys of more KV heads than stay in L2 together: heads run in groups, and
+    rows are checked here and there."""
+    import query_aware_sparse_gb300 as qs
+    h, d, S, L = 9, 128, 16, 17003
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    pages = -(-L // S)
+    kp = torch.randn((pages, h, S, d), generator=g, device="cuda").half()
+    vp = torch.randn((pages, h, S, d), generator=g, device="cuda").half()
+    cache = qs.PagedCache(kp, vp, torch.zeros((pages, h, 2, d), dtype=F16, device="cuda"))
+    ids = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+    table = qs.PageTable(dev_i32([0, pages]), ids, dev_i32([L]))
+    q = torch.randn((rows, h, d), generator=g, device="cuda").half()
+    out, lse = qs.prefill_attn(cache, table, q, 1, dev_i32([0, rows]), mods=qs.ScoreMods(window=window))
+    k = kp[ids.long()].transpose(1, 2).reshape(-1, h, d)[:L].double()
+    v = vp[ids.long()].transpose(1, 2).reshape(-1, h, d)[:L].double()
+    for i in (0, 1, 127, 128, 255, 256, 511, rows - 2, rows - 1):
+        p = L - rows + i
+        lo = max(0, p - window + 1) if window else 0
+        x = torch.einsum("hd,jhd->hj", q[i].double(), k[lo:p + 1]) / d ** 0.5
+        z = torch.logsumexp(x, 1)
+        w = torch.exp(x - z[:, None])
+        o = torch.einsum("hj,jhd->hd", w, v[lo:p + 1])
+        mean = torch.einsum("hj,jhd->hd", w, v[lo:p + 1].abs())
+        # weights and output each rounded to fp16; logits to 132 roundings of sum |q k| / sqrt(d)
+        # (about 7: 5.6e-5, twice in a weight), 1127 roundings of 2^-24 in a row's sums (6.7e-5)
+        assert ((out[i].double() - o).abs() <= mean * (HALF16 + 2e-4) + o.abs() * HALF16 + 1e-7).all(), i
+        assert ((lse[i].double() - z).abs() <= 1e-4).all(), i
+    assert qs.device_error() == 0
+
+
 def test_prefill_large_scores():
     case = _rows_case(62, [900], [300], h_kv=1, group=2, d=64, S=16)
     case["q"] = (case["q"] * 0 + 8).half()

@@ -125,6 +125,14 @@ def test_append_one_token_and_decode_batch():
     _check(7, [1] * 75, rng.integers(0, 50, 75).tolist(), h=2, group=1, d=64)
 
 
+def test_append_many_pages_of_few_heads():
+    """Enough pages to fill the device several times over, from one request and
+    from hundreds."""
+    _check(17, [10007], [5], h=1, group=1)
+    rng = np.random.default_rng(4)
+    _check(18, rng.integers(0, 3, 800).tolist(), rng.integers(0, 40, 800).tolist(), h=1, group=2, d=64)
+
+
 def test_append_without_queries():
     _check(8, LENS, BEFORE, with_q=False)
 
