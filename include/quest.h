@@ -476,7 +476,8 @@ typedef struct quest_score_mods {
  *   workspace : device, >= quest_dense_decode_workspace_size(...) bytes, 16-B
  *               aligned; nothing in it has to be set or kept. Calls that share
  *               a workspace must not overlap on the GPU.
- * At most 524288 requests (else QUEST_ERR_UNSUPPORTED).
+ * At most 524288 requests, and pools of less than 2^31 rows (n_phys * h_kv *
+ * page_size), else QUEST_ERR_UNSUPPORTED.
  * A page outside the pool is skipped (QUEST_DEVERR_PAGE_RANGE), a request's
  * tokens beyond its page table too (QUEST_DEVERR_TABLE_RANGE). Keys and values
  * of the seq_lens[r] valid tokens must be finite, also where a query does not
@@ -511,7 +512,8 @@ QUEST_API size_t quest_dense_decode_workspace_size(int32_t batch, int32_t nnz, i
  *   workspace: device, >= quest_prefill_workspace_size(...) bytes, 16-B
  *              aligned; as in quest_dense_decode_attn
  * fp16: the products run on the tensor cores with fp32 accumulation, softmax
- * weights rounded to fp16. Errors and finiteness as quest_dense_decode_attn.
+ * weights rounded to fp16. Errors, finiteness and pool rows as
+ * quest_dense_decode_attn.
  */
 QUEST_API quest_status quest_prefill_attn(const quest_cache* cache, const quest_pages* pages,
                                           const void* q, int32_t group, const int32_t* q_indptr,
@@ -552,7 +554,8 @@ QUEST_API int32_t quest_set_trace(void* device_buffer, int32_t max_ctas, int32_t
  * quest_sparse_decode_attn(_noalloc) and quest_union_decode_attn calls, the
  * first copy slot of warp 0 of the first CTA expects 16 bytes more than its
  * copies bring; in later quest_dense_decode_attn and (fp16)
- * quest_prefill_attn calls likewise, and there every wait of that CTA gives up. Either way that wait runs out: the kernel sets
+ * quest_prefill_attn calls likewise, and there every wait of that CTA gives
+ * up. Either way that wait runs out: the kernel sets
  * QUEST_DEVERR_WAIT_TIMEOUT, issues no further copies, waits (bounded) for
  * those in flight and returns, its outputs unspecified; the device stays
  * usable. wait_limit: tries of every bounded in-kernel wait of those calls

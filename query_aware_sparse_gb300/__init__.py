@@ -153,6 +153,12 @@ def dtype_code(dt: torch.dtype) -> int:
     raise ValueError(f"unsupported element type {dt}")
 
 
+def _common_device(*tensors) -> int:
+    """The CUDA device index that all have, else -1."""
+    dev = tensors[0].get_device()
+    return dev if all(t.get_device() == dev for t in tensors) else -1
+
+
 class PagedCache:
     """One layer's pool + summary (caller-owned torch tensors).
 
@@ -167,6 +173,7 @@ class PagedCache:
         n_phys, h_kv, S, d = k_pool.shape
         self.n_phys, self.h_kv, self.page_size, self.head_dim = n_phys, h_kv, S, d
         self.dtype = k_pool.dtype
+        self.device_index = _common_device(k_pool, v_pool, summary)
         self.summary_fp8 = summary.dtype == torch.uint8
         if not self.summary_fp8 and summary.dtype != k_pool.dtype:
             raise ValueError("summary must have the K/V dtype or be uint8 E4M3 codes")
@@ -188,6 +195,7 @@ class PageTable:
 
     def __init__(self, page_indptr, page_indices, seq_lens, nnz=None):
         self.page_indptr, self.page_indices, self.seq_lens = page_indptr, page_indices, seq_lens
+        self.device_index = _common_device(page_indptr, page_indices, seq_lens)
         self.batch = int(seq_lens.shape[0])
         self.nnz = int(page_indices.shape[0]) if nnz is None else int(nnz)
         self.c = QuestPages(page_indptr.data_ptr(), page_indices.data_ptr(),
@@ -399,16 +407,40 @@ def _expect_rows(name, t, dtype, shape, device) -> int:
                      f"rows, not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
 
 
-def _current(cache: PagedCache) -> int:
-    """Index of the current device, which has to hold the cache."""
-    dev = cache.k_pool.get_device()
+def _current(cache: PagedCache, table: PageTable) -> int:
+    """Index of the current device, which has to hold the cache and its page table."""
+    dev = cache.device_index
     if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"the cache must be on the current CUDA device, not {cache.k_pool.device}")
+    if table.device_index != dev:
+        raise ValueError(f"the page table must be on CUDA device {dev}, not {table.seq_lens.device}")
     return dev
 
 
 def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream must be of CUDA device {dev}, not {stream.device_index}")
+    return stream.cuda_stream
+
+
+def _result(shape, dtype, dev, stream):
+    """Memory for a result that ``stream`` writes: taken from that stream, so no
+    earlier work of the current one still uses it, and kept, when it is
+    released, until the current stream has read it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _expect_workspace(t, device):
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous on CUDA device {device}, not on {t.device} "
+                         f"with strides {t.stride()}")
 
 
 def _scratch(n, dev, stream):
@@ -425,7 +457,7 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
     rotated (q may be None). Tokens may be strided (the parts of one fused
     projection); inv_freq is fp64 [rotary_dim / 2] (see rope_frequencies);
     positions int32 [n_new] replaces the tokens' places in the cache."""
-    dev, dt, n = _current(cache), cache.dtype, k_new.shape[0]
+    dev, dt, n = _current(cache, table), cache.dtype, k_new.shape[0]
     h, d = cache.h_kv, cache.head_dim
     kv = (n, h, d)
     k_stride = _expect_rows("k_new", k_new, dt, kv, dev)
@@ -440,7 +472,7 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
         rows = (n, h * group, d)
         q_stride = _expect_rows("q", q, dt, rows, dev)
         if q_out is None:
-            q_out = torch.empty(rows, dtype=dt, device=dev)
+            q_out = _result(rows, dt, dev, stream)
         _expect("q_out", q_out, dt, rows, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -460,6 +492,8 @@ class ScoreMods:
     def __init__(self, softcap: float = 0.0, window: int = 0, alibi_slopes=None, doc_starts=None,
                  prefix_lens=None):
         self.softcap, self.window = float(softcap), int(window)
+        if abs(self.window) >= 1 << 31:
+            raise ValueError("window must fit 32 bits")
         self.alibi_slopes, self.doc_starts, self.prefix_lens = alibi_slopes, doc_starts, prefix_lens
         self.c = QuestScoreMods(_ptr(alibi_slopes), _ptr(doc_starts), _ptr(prefix_lens),
                                 self.softcap, self.window)
@@ -484,13 +518,13 @@ def dense_decode_attn(cache: PagedCache, table: PageTable, q, group: int, out=No
     """quest_dense_decode_attn: (out [B, h_q, d] fp32, lse [B, h_q] fp32) of one
     query per request over all of its cached tokens. ``workspace``: uint8,
     dense_decode_workspace_size bytes."""
-    dev, h_q, d = _current(cache), cache.h_kv * group, cache.head_dim
+    dev, h_q, d = _current(cache, table), cache.h_kv * group, cache.head_dim
     B = table.batch
     _expect("q", q, cache.dtype, (B, h_q, d), dev)
     if out is None:
-        out = torch.empty((B, h_q, d), dtype=torch.float32, device=dev)
+        out = _result((B, h_q, d), torch.float32, dev, stream)
     if lse is None:
-        lse = torch.empty((B, h_q), dtype=torch.float32, device=dev)
+        lse = _result((B, h_q), torch.float32, dev, stream)
     _expect("out", out, torch.float32, (B, h_q, d), dev)
     _expect("lse", lse, torch.float32, (B, h_q), dev)
     if mods is not None:
@@ -499,6 +533,7 @@ def dense_decode_attn(cache: PagedCache, table: PageTable, q, group: int, out=No
         n = dense_decode_workspace_size(B, table.nnz, cache.h_kv, group, d, cache.page_size,
                                         cache.dtype)
         workspace = _scratch(n, dev, stream)
+    _expect_workspace(workspace, dev)
     _check(lib().quest_dense_decode_attn(
         ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q), int(group),
         None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
@@ -518,14 +553,14 @@ def prefill_attn(cache: PagedCache, table: PageTable, q, group: int, q_indptr, o
     fp32) of each request's last tokens, rows q_indptr[r] .. q_indptr[r + 1] of
     q, over its cached tokens. ``workspace``: uint8, prefill_workspace_size
     bytes."""
-    dev, h_q, d = _current(cache), cache.h_kv * group, cache.head_dim
+    dev, h_q, d = _current(cache, table), cache.h_kv * group, cache.head_dim
     n = q.shape[0]
     _expect("q", q, cache.dtype, (n, h_q, d), dev)
     _expect("q_indptr", q_indptr, torch.int32, (table.batch + 1,), dev)
     if out is None:
-        out = torch.empty((n, h_q, d), dtype=cache.dtype, device=dev)
+        out = _result((n, h_q, d), cache.dtype, dev, stream)
     if lse is None:
-        lse = torch.empty((n, h_q), dtype=torch.float32, device=dev)
+        lse = _result((n, h_q), torch.float32, dev, stream)
     _expect("out", out, cache.dtype, (n, h_q, d), dev)
     _expect("lse", lse, torch.float32, (n, h_q), dev)
     if mods is not None:
@@ -534,6 +569,7 @@ def prefill_attn(cache: PagedCache, table: PageTable, q, group: int, q_indptr, o
         size = prefill_workspace_size(table.batch, n, table.nnz, cache.h_kv, group, d,
                                       cache.page_size, cache.dtype)
         workspace = _scratch(size, dev, stream)
+    _expect_workspace(workspace, dev)
     _check(lib().quest_prefill_attn(
         ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q), int(group), _ptr(q_indptr), int(n),
         None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),

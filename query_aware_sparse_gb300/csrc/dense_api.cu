@@ -30,6 +30,12 @@ bool valid_shape(int32_t h_kv, int32_t group, int32_t head_dim, int32_t page_siz
          (page_size == 16 || page_size == 32) && (dtype == QUEST_F16 || dtype == QUEST_F32);
 }
 
+// The attention kernels name a pool's rows (one token of one KV head) by the
+// signed 32-bit coordinate of a tensor map.
+bool addressable(const quest_cache* c) {
+  return (int64_t)c->n_phys * c->h_kv <= INT32_MAX / c->page_size;
+}
+
 quest::DenseArgs dense_args(const quest_cache* cache, const quest_pages* pages, const void* q,
                             int32_t group, const quest_score_mods* mods, void* out, float* lse,
                             float sm_scale, void* workspace) {
@@ -114,6 +120,7 @@ quest_status quest_dense_decode_attn(const quest_cache* cache, const quest_pages
   if ((st = check_pages(pages, true)) != QUEST_OK) return st;
   if (!valid_group(group)) return QUEST_ERR_UNSUPPORTED;
   if ((st = check_mods(mods)) != QUEST_OK) return st;
+  if (!addressable(cache)) return QUEST_ERR_UNSUPPORTED;
   if (pages->batch == 0) return QUEST_OK;
   if (pages->batch > quest::kDecodeMaxBatch) return QUEST_ERR_UNSUPPORTED;
   if (!q || !out || !aligned16(q) || !aligned16(out)) return QUEST_ERR_INVALID_ARG;
@@ -144,6 +151,7 @@ quest_status quest_prefill_attn(const quest_cache* cache, const quest_pages* pag
   if ((st = check_pages(pages, true)) != QUEST_OK) return st;
   if (!valid_group(group)) return QUEST_ERR_UNSUPPORTED;
   if ((st = check_mods(mods)) != QUEST_OK) return st;
+  if (!addressable(cache)) return QUEST_ERR_UNSUPPORTED;
   if (n_q < 0) return QUEST_ERR_INVALID_ARG;
   if (pages->batch == 0 || n_q == 0) return QUEST_OK;
   if (!q || !q_indptr || !out || !aligned16(q) || !aligned16(out)) return QUEST_ERR_INVALID_ARG;

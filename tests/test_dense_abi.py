@@ -171,6 +171,53 @@ def test_binding_refuses_tensors(q):
         m.check(2, 1, 1, dev)
 
 
+def test_binding_refuses_places(q, monkeypatch):
+    """Streams, workspaces and page tables of another device; windows beyond 32 bits."""
+    class Stream:
+        device_index, cuda_stream = 1, 77
+    assert q._raw_stream(Stream, 1) == 77
+    with pytest.raises(ValueError, match="stream must be"):
+        q._raw_stream(Stream, 0)
+    ws = torch.zeros(64, dtype=torch.uint8)
+    q._expect_workspace(ws, ws.get_device())
+    for bad, dev in ((ws, 0), (ws[::2], ws.get_device())):
+        with pytest.raises(ValueError, match="workspace must be"):
+            q._expect_workspace(bad, dev)
+    class On:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def get_device(self):
+            return self.dev
+    assert q._common_device(On(1), On(1), On(1)) == 1
+    assert q._common_device(On(0), On(1), On(0)) == q._common_device(On(0), On(0), On(-1)) == -1
+    pool = torch.zeros((1, 1, 16, 64), dtype=torch.float16)
+    cache, i32 = q.PagedCache(pool, pool, pool[:, :, :2]), torch.tensor([0, 1], dtype=torch.int32)
+    table = q.PageTable(i32, i32[:1], i32[1:])
+    assert cache.device_index == table.device_index == -1
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    cache.device_index = 0
+    with pytest.raises(ValueError, match="page table must be"):
+        q._current(cache, table)
+    table.device_index = 0
+    assert q._current(cache, table) == 0
+    for bad in (1 << 31, (1 << 32) + 5, -(1 << 31)):
+        with pytest.raises(ValueError, match="window"):
+            q.ScoreMods(window=bad)
+    assert q.ScoreMods(window=(1 << 31) - 1).c.window == (1 << 31) - 1
+
+
+def test_attention_refuses_pools_beyond_a_coordinate(q):
+    by, L, p = ctypes.byref, q.lib(), _pages(q)
+    rows = (1 << 31) // 16
+    for n, h, refused in ((rows // 2, 2, True), (rows // 2 - 1, 2, False), (1 << 30, 1 << 20, True)):
+        c = _cache(q, n=n, h=h)
+        got = (L.quest_dense_decode_attn(by(c), by(p), FAKE, 4, None, FAKE, FAKE, F, None, 0, None),
+               L.quest_prefill_attn(by(c), by(p), None, 4, FAKE, 3, None, FAKE, FAKE, F, FAKE, 1 << 30, None))
+        want = (UNSUPPORTED, UNSUPPORTED) if refused else (WORKSPACE, INVALID)
+        assert got == want, (n, h)
+
+
 def test_frequencies(q):
     f = q.rope_frequencies(64, base=500000.0, device="cpu")
     assert f.dtype == torch.float64 and f.shape == (32,)

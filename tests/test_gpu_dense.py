@@ -341,6 +341,41 @@ def test_two_calls_at_once():
         assert all(torch.equal(x, y) for x, y in zip(want, g))
 
 
+def test_results_of_another_stream():
+    """A call on a side stream does not write into memory that the current stream
+    gave back while its work on it was still to come."""
+    import query_aware_sparse_gb300 as q
+    torch.manual_seed(11)
+    cache = q.PagedCache(*(torch.randn(64, 2, 16, 128, device="cuda", dtype=torch.float16) for _ in range(2)),
+                         torch.empty(64, 2, 2, 128, device="cuda", dtype=torch.float16))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = q.PageTable(torch.tensor([0, 64], **i32), torch.arange(64, **i32), torch.tensor([1000], **i32))
+    x = torch.randn(300, 8, 128, device="cuda", dtype=torch.float16)
+    rows = torch.tensor([0, 300], **i32)
+    kv, before = x[:, :2].contiguous(), torch.tensor([700], **i32)
+    freq, side = q.rope_frequencies(128), torch.cuda.Stream()
+
+    def calls(stream):
+        # (the append comes last: it changes what the others read)
+        yield lambda: q.dense_decode_attn(cache, table, x[:1], 4, stream=stream)
+        yield lambda: q.prefill_attn(cache, table, x, 4, rows, stream=stream)
+        yield lambda: (q.rope_append_kv(cache, table, x, kv, kv, rows, before, freq, 4, stream=stream),)
+    for plain, other in zip(calls(None), calls(side)):
+        want = plain()
+        want = [w.clone() for w in want]
+        other()                                        # (loads what the call needs)
+        torch.cuda.synchronize()
+        junk = [torch.empty_like(w) for w in want]
+        torch.cuda._sleep(20_000_000)
+        for j in junk:
+            j.fill_(7.0)
+        del junk, j
+        got = other()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+
+
 def test_requests_that_share_pages():
     """The same physical pages as the prefix of two requests, and twice in one."""
     import query_aware_sparse_gb300 as qs
