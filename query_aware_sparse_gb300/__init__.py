@@ -456,7 +456,8 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
     v_new, updates the summaries, and returns q [n_new, h_kv * group, d]
     rotated (q may be None). Tokens may be strided (the parts of one fused
     projection); inv_freq is fp64 [rotary_dim / 2] (see rope_frequencies);
-    positions int32 [n_new] replaces the tokens' places in the cache."""
+    positions int32 [n_new] replaces the tokens' places in the cache. In a loop
+    of small calls pass q_out: its allocation is 6 of their 15 us on the host."""
     dev, dt, n = _current(cache, table), cache.dtype, k_new.shape[0]
     h, d = cache.h_kv, cache.head_dim
     kv = (n, h, d)
@@ -479,8 +480,8 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
     rope = QuestRope(_ptr(inv_freq), _ptr(positions), 2 * inv_freq.numel(), int(bool(interleaved)))
     _check(lib().quest_rope_append_kv(
         ctypes.byref(cache.c), ctypes.byref(table.c), ctypes.byref(rope), _ptr(q), _ptr(k_new),
-        _ptr(v_new), q_stride, k_stride, v_stride, n, int(group), _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out),
-        _raw_stream(stream, dev)))
+        _ptr(v_new), q_stride, k_stride, v_stride, n, int(group), _ptr(append_indptr),
+        _ptr(seq_lens_before), _ptr(q_out), _raw_stream(stream, dev)))
     return q_out
 
 
