@@ -140,7 +140,10 @@ cudaError_t launch_prefill(const DenseArgs& a, cudaStream_t s) {
                                 a.window);
     if (w.bytes <= plan.bytes) plan = w;
   }
-  const PrefillArgs p = prefill_args(a, plan);
+  PrefillArgs p = prefill_args(a, plan);
+  // fp16 q.k stay below 65504^2 * 128 < 2^39. Where no logit can pass 2^-13 of the
+  // cap, cap tanh(x / cap) = x (1 - (x / cap)^2 / 3 ..) is x to 2^-27 of itself.
+  if (a.dtype == QUEST_F16 && a.softcap >= 0x1p52f * a.scale) p.a.softcap = 0.f;
   return a.dtype == QUEST_F16 ? launch_f16(p, plan.tiles, s) : launch_prefill_f32(p, s);
 }
 

@@ -56,51 +56,74 @@ template <int D, int TILES> struct PrefillShape {
   static constexpr int PER_SM = TILES == 2 ? 1 : 2;
 };
 
-// x -> 2 tanh(y / 2), y = x * to_y. Two ways that use different pipes:
-// 2 - 4 / (1 + e^y), two values sharing one reciprocal, to 4e-7; and
-// y (1 + y^2 R(y^2)), fitted at Chebyshev nodes for |y| < 2, to 1.1e-7 of
-// itself. While all of a warp's |y| are below 2 (bit 30 of an fp32 number says
-// so), kPolyPairs pairs of eight take the polynomial. A 2048-token chunk over
-// 65536 capped keys with 32 heads takes 2.38, 2.30, 2.29, 2.28 and 2.60 ms with
-// 0, 3, 4, 6 and 8 of them: six, the more exact of the fast ones. Otherwise
-// every value takes the first way by itself.
-constexpr int kPolyPairs = 6;
-template <int N> __device__ __forceinline__ void double_tanh(float (&x)[N], float to_y) {
-  uint32_t bits = 0;
+// x -> 4 tanh(t / 4), t = x * to_t: t is four times the logit over its cap. The error
+// goes with the value, not with the cap, as far as a weight can feel it. By the
+// largest |t| of a warp's rows:
+//   below 2, below 4: t (1 + w R(w)), w = t^2, to 2 units of 2^-24 of the result;
+//   caps up to kSmallCap: 4 - 8 / (1 + e^(t / 2)), off by 2^-19 at most: 2^-21 of the
+//     cap, 2^-15 in a logit, little next to the rounding of the weights (2^-11);
+//   larger caps: t N(w) / D(w), all coefficients positive, to 12 units of the
+//     result, |t| held at 32, where tanh is 1 to 4 units: the small logits of rows
+//     next to ones near a large cap keep their accuracy.
+// R, N and D fitted at Chebyshev nodes. 2048 tokens over 65536 keys, 32 heads, d 128:
+// 2.03, 2.75, 3.00 and 3.58 ms. Blocks where a row's keys begin or end (`edge`) take
+// one of the last two, value by value the same whatever hidden columns hold; rows
+// that are not `live` have no say.
+constexpr float kSmallCap = 64.f;
+template <int N> __device__ __forceinline__ void four_tanh(float (&x)[N], float to_t, bool small, bool live, bool edge) {
+  float most = 0.f;
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
-    const float2 y = mul2(make_float2(x[c], x[c + 1]), both(to_y));
-    x[c] = y.x;
-    x[c + 1] = y.y;
-    bits |= __float_as_uint(y.x) | __float_as_uint(y.y);
+    const float2 t = mul2(make_float2(x[c], x[c + 1]), both(to_t));
+    x[c] = t.x;
+    x[c + 1] = t.y;
+    most = fmaxf(fmaxf(most, fabsf(t.x)), fabsf(t.y));
   }
-  if (__all_sync(FULL, (bits & 0x40000000u) == 0)) {
+  if (!edge && __all_sync(FULL, most < 2.f || !live)) {
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
-      const float2 y = make_float2(x[c], x[c + 1]);
-      float2 v;
-      if (c / 2 % 8 < kPolyPairs) {
-        const float2 w = mul2(y, y);
-        v = fma2(w, both(-2.5863442942863912e-08f), both(6.151556135591818e-07f));
-        v = fma2(v, w, both(-8.036506187636405e-06f));
-        v = fma2(v, w, both(8.463124686386436e-05f));
-        v = fma2(v, w, both(-0.00084275146946311f));
-        v = fma2(v, w, both(0.008333212696015835f));
-        v = fma2(v, w, both(-0.0833333283662796f));
-        v = fma2(v, w, both(1.f));
-        v = mul2(v, y);
-      } else {
-        v = mul2(y, both(LOG2E));
-        v = add2(make_float2(ex2(v.x), ex2(v.y)), both(1.f));
-        const float r = rcp(v.x * v.y);
-        v = fma2(make_float2(r * v.y, r * v.x), both(-4.f), both(2.f));
-      }
+      const float2 t = make_float2(x[c], x[c + 1]), w = mul2(t, t);
+      float2 v = fma2(w, both(2.744864673331904e-07f), both(-1.3033962204644922e-05f));
+      v = fma2(v, w, both(0.0005207217182032764f));
+      v = fma2(v, w, both(-0.020833319053053856f));
+      v = fma2(v, w, both(1.f));
+      v = mul2(v, t);
       x[c] = v.x;
       x[c + 1] = v.y;
     }
+  } else if (!edge && __all_sync(FULL, most < 4.f || !live)) {
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      const float2 t = make_float2(x[c], x[c + 1]), w = mul2(t, t);
+      float2 v = fma2(w, both(-1.5672128308649724e-12f), both(1.4963504046949794e-10f));
+      v = fma2(v, w, both(-7.838174553853605e-09f));
+      v = fma2(v, w, both(3.3050713454940706e-07f));
+      v = fma2(v, w, both(-1.3167673387215473e-05f));
+      v = fma2(v, w, both(0.0005208253278397024f));
+      v = fma2(v, w, both(-0.0208333320915699f));
+      v = fma2(v, w, both(1.f));
+      v = mul2(v, t);
+      x[c] = v.x;
+      x[c + 1] = v.y;
+    }
+  } else if (small) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x[c] = fmaf(rcp(1.f + ex2(x[c] * (0.5f * LOG2E))), -8.f, 4.f);
   } else {
 #pragma unroll
-    for (int c = 0; c < N; ++c) x[c] = fmaf(rcp(1.f + ex2(x[c] * LOG2E)), -4.f, 2.f);
+    for (int c = 0; c < N; c += 2) {
+      const float2 t = make_float2(clamp_nan(x[c], 32.f), clamp_nan(x[c + 1], 32.f)), w = mul2(t, t);
+      float2 n = fma2(w, both(2.80596501589514e-09f), both(1.1560538951016497e-05f));
+      n = fma2(n, w, both(0.008084234781563282f));
+      n = fma2(n, w, both(1.f));
+      float2 d = fma2(w, both(3.777043348224263e-12f), both(5.8521202106476267e-08f));
+      d = fma2(d, w, both(9.317861258750781e-05f));
+      d = fma2(d, w, both(0.028917556628584862f));
+      d = fma2(d, w, both(1.f));
+      n = mul2(mul2(n, t), make_float2(rcp(d.x), rcp(d.y)));
+      x[c] = n.x;
+      x[c + 1] = n.y;
+    }
   }
 }
 
@@ -375,7 +398,9 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     const bool valid = tok < n_r && row0 + tok < a.n_q;
     Seen seen{0, 0};
     if (valid) seen = seen_keys(pos, held, a.window, a.doc_starts ? a.doc_starts[row0 + tok] : 0, prefix);
-    if (seen.hi <= seen.lo) seen = Seen{0, 0};
+    // A row that sees nothing, or is none, is not looked at: its weights may be
+    // anything, they reach no other row, and its l is taken as 0 at the end.
+    const bool live = seen.hi > seen.lo;
     // pages outside the pool: reported, and looked for block by block if any
     for (int pg = (n0 * BN >> page_shift) + (int)threadIdx.x; pg < min(n1 * BN, held + S - 1) >> page_shift;
          pg += TILES * 128) {
@@ -388,10 +413,10 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16;
     const int h = g * G + row % G;
     const float log2s = a.scale * LOG2E;
-    const float half_cap2 = 0.5f * a.softcap * LOG2E, to_y = CAP ? 2.f * a.scale / a.softcap : 0.f;
+    const float cap2_4 = 0.25f * a.softcap * LOG2E, to_t = CAP ? 4.f * a.scale / a.softcap : 0.f;
     const float slope2 = ALIBI && valid ? a.slopes[h] * LOG2E : 0.f;
-    const float sl2 = ALIBI ? 1.f : CAP ? half_cap2 : log2s;   // of the value the maximum is taken of
-    float m = seen.hi > 0 ? -INFINITY : 0.f, l = 0.f;  // a row that sees nothing needs no maximum
+    const float sl2 = ALIBI ? 1.f : CAP ? cap2_4 : log2s;   // of the value the maximum is taken of
+    float m = live ? -INFINITY : 0.f, l = 0.f;
     uint32_t s_phase = 0;                             // a bit per S buffer
     bool ok = true;
     const int first = tile == 0 ? t0[0] : t0[TILES - 1], last = tile == 0 ? t1[0] : t1[TILES - 1];
@@ -418,17 +443,19 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
 #pragma unroll
       for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
       const int kb = n * BN;
-      if (CAP) double_tanh<BN>(x, to_y);
+      const bool edge = __any_sync(FULL, live && (kb < seen.lo || kb + BN > seen.hi || bad));
+      auto hidden = [&](int c) { return kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1); };
+      if (CAP) four_tanh<BN>(x, to_t, a.softcap <= kSmallCap, live, edge);
       if (ALIBI) {
         const float d0 = (float)(pos - kb);
 #pragma unroll
         for (int c = 0; c < BN; ++c)
-          x[c] = fmaf(fabsf(d0 - (float)c), -slope2, x[c] * (CAP ? half_cap2 : log2s));
+          x[c] = fmaf(fabsf(d0 - (float)c), -slope2, x[c] * (CAP ? cap2_4 : log2s));
       }
-      if (__any_sync(FULL, kb < seen.lo || kb + BN > seen.hi || bad)) {
+      if (edge) {
 #pragma unroll
         for (int c = 0; c < BN; ++c)
-          if (kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1)) x[c] = -INFINITY;
+          if (hidden(c)) x[c] = -INFINITY;
       }
       // The maximum lags: with it the block's weights, and only where their sum
       // passes 2^15 (one above 2^14 is among them, or many above 2^8) or a row
@@ -483,7 +510,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
         }
         sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
         if (once) break;
-        again = __any_sync(FULL, sum > 32768.f);
+        again = __any_sync(FULL, live && sum > 32768.f);
         if (!again) break;
       }
       if (!ok) break;
@@ -502,8 +529,9 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       ok = warp_wait_or_quit(&o_full[tile], 0, p.wait_limit, &s_quit);
     if (ok) {
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m - 6.f + lg2(l) : -INFINITY;
+      const bool some = live && l > 0.f;               // has a key
+      const float inv = some ? 1.f / l : 0.f;
+      const float lse2 = some ? m - 6.f + lg2(l) : -INFINITY;
       const size_t at = ((size_t)row0 + tok) * hq + h;
       const size_t part = (size_t)split * a.n_q * hq + at;
 #pragma unroll 1
@@ -516,7 +544,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          o[e] = last > first ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          o[e] = some ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
         if (p.splits > 1) {
           float* dst = p.part_o + part * D + c * 32;
           if (valid) {

@@ -227,6 +227,12 @@ template <int N> __device__ __forceinline__ void regs_up() {
 template <int N> __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
+// x held to -most .. most; NaN stays.
+__device__ __forceinline__ float clamp_nan(float x, float most) {
+  float y;
+  asm("{\n\t.reg .f32 a;\n\tmin.NaN.f32 a, %1, %2;\n\tmax.NaN.f32 %0, a, %3;\n\t}" : "=f"(y) : "f"(x), "f"(most), "f"(-most));
+  return y;
+}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
