@@ -31,10 +31,10 @@ __device__ __forceinline__ int held_tokens(int len, int table_pages, int page_si
 // cap tanh(x / cap): for |x| < cap the product of x and a polynomial in
 // (x / cap)^2 (tanh(u) / u fitted at Chebyshev nodes for |u| < 1, 1.1e-7 of
 // itself off at most, so small logits keep their relative accuracy), else
-// tanhf. Converged warps only.
+// tanhf. Which of the two a value takes goes by itself alone; a warp without a
+// large one skips tanhf. Converged warps only.
 __device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
   const float u = x * inv_cap;
-  if (__any_sync(FULL, !(fabsf(u) < 1.f))) return cap * tanhf(u);
   const float w = u * u;
   float q = -0.00042374664917588234f;
   q = fmaf(q, w, 0.0025196773931384087f);
@@ -43,7 +43,9 @@ __device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
   q = fmaf(q, w, -0.05393609404563904f);
   q = fmaf(q, w, 0.13333140313625336f);
   q = fmaf(q, w, -0.3333333134651184f);
-  return x * fmaf(q, w, 1.f);
+  float y = x * fmaf(q, w, 1.f);
+  if (__any_sync(FULL, !(fabsf(u) < 1.f))) y = fabsf(u) < 1.f ? y : cap * tanhf(u);
+  return y;
 }
 
 }  // namespace quest

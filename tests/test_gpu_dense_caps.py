@@ -93,6 +93,22 @@ def test_prefill_caps_f32(d):
         _compare(case, out, lse, np.arange(790), cap, 2.0 ** -22)
 
 
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_caps(d, dtype):
+    """The same logits from the call of one new token."""
+    import query_aware_sparse_gb300 as qs
+    case = _case("one", d, dtype, 320 + d)
+    cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(case["table"])
+    for cap in CAPS:
+        for last in ([699, 789], [13, 710], [200, 750]):
+            lens = np.asarray([last[0] + 1, last[1] - 699], np.int32)
+            out, lse = qs.dense_decode_attn(cache, gpu_table(case["table"], seq_lens=lens), case["q"][last].cuda(), 2,
+                                            mods=qs.ScoreMods(softcap=cap, window=1))
+            _compare(case, out, lse, np.asarray(last), cap, 2.0 ** -22)
+    assert qs.device_error() == 0
+
+
 @pytest.mark.parametrize("alibi", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("L,rows,group,cut", [(704, 704, 2, False), (6016, 33, 4, True), (8320, 8320, 8, False),

@@ -48,10 +48,16 @@ def _prefill(case, cache, table, q, mods):
     return qs.prefill_attn(cache, table, q, 2, dev_i32(case["q_indptr"]), mods=mods)
 
 
+def _decode(case, cache, table, q, mods):
+    import query_aware_sparse_gb300 as qs
+    last = torch.as_tensor(case["q_indptr"][1:] - 1, device="cuda").long()
+    return qs.dense_decode_attn(cache, table, q[last].contiguous(), 2, mods=mods)
+
+
 @pytest.mark.parametrize("dtype", [F16, F32])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("kw", MODS)
-@pytest.mark.parametrize("call", [_prefill])
+@pytest.mark.parametrize("call", [_prefill, _decode])
 def test_slots_without_a_token(call, kw, d, dtype):
     import query_aware_sparse_gb300 as qs
     case = _rows_case(401, LENS, ROWS, h_kv=2, group=2, d=d, S=16, dtype=dtype)
