@@ -511,8 +511,10 @@ QUEST_API size_t quest_dense_decode_workspace_size(int32_t batch, int32_t nnz, i
  *   lse      : device fp32 [n_q, h_kv * group], or NULL
  *   workspace: device, >= quest_prefill_workspace_size(...) bytes, 16-B
  *              aligned; as in quest_dense_decode_attn
- * fp16: the products run on the tensor cores with fp32 accumulation, softmax
- * weights rounded to fp16. Errors, finiteness and pool rows as
+ * fp16: the products run on the tensor cores, softmax weights rounded to fp16.
+ * Their accumulators truncate, so a row's sums over more than 8192 keys are held
+ * in fp32 in the workspace meanwhile (tables of more tokens need one of a fp32
+ * output's size at least); what is left is 2^-13 of an output. Errors, finiteness and pool rows as
  * quest_dense_decode_attn.
  */
 QUEST_API quest_status quest_prefill_attn(const quest_cache* cache, const quest_pages* pages,

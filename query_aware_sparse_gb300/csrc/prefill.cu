@@ -22,6 +22,7 @@ namespace {
 
 struct Plan {
   int tiles, blocks, splits, near_heads;
+  bool chained;
   size_t lse_at, bytes;               // of the partial results in the workspace
 };
 
@@ -29,7 +30,7 @@ struct Plan {
 // device), so it goes by their mean. window: 0, or the keys a row sees at most.
 Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t group,
                   int32_t head_dim, int32_t page_size, int32_t dtype, int32_t window) {
-  Plan p{1, 0, 1, h_kv, 0, 16};
+  Plan p{1, 0, 1, h_kv, false, 0, 16};
   if (n_q == 0 || batch == 0) return p;
   const bool f16 = dtype == QUEST_F16;
   const long long all_keys = (long long)nnz * page_size;
@@ -88,7 +89,8 @@ Plan plan_prefill(int32_t batch, int32_t n_q, int32_t nnz, int32_t h_kv, int32_t
       p.splits = s;
     }
   }
-  if (p.splits > 1) {
+  p.chained = f16 && all_keys > kChainKeys;
+  if (p.splits > 1 || p.chained) {
     const size_t all = (size_t)p.splits * n_q * h_kv * group;
     p.lse_at = all * head_dim * sizeof(float);
     p.bytes = p.lse_at + all * sizeof(float);
@@ -102,6 +104,7 @@ PrefillArgs prefill_args(const DenseArgs& a, const Plan& plan) {
   p.blocks = plan.blocks;
   p.splits = plan.splits;
   p.near_heads = plan.near_heads;
+  p.chained = plan.chained;
   p.part_o = static_cast<float*>(a.workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + plan.lse_at);
   p.wait_limit = wait_limit();

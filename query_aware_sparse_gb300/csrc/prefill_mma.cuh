@@ -10,7 +10,8 @@
 // usual block so needs no maximum at all, and no weight passes fp16's 65504;
 // the factor 2^6 keeps small weights out of fp16's subnormal range. P is
 // rounded to fp16 (half a step, 2^-11 of itself) because the second product
-// takes fp16 operands; S, O, m and l stay in fp32.
+// takes fp16 operands; S, m and l stay in fp32, O for kChainKeys keys in the tensor
+// core's accumulator, then in fp32.
 //
 // Bound. 4 D flops per (row, visible key) on tcgen05 against 2 D bytes per key
 // and KV head: tensor bound from a few hundred rows on. The softmax runs one
@@ -54,6 +55,8 @@ template <int D, int TILES> struct PrefillShape {
   static constexpr uint32_t O_COL = TILES * SBUF * BN;         // S buffers first
   static constexpr uint32_t TMEM = O_COL + TILES * D <= 128 ? 128 : O_COL + TILES * D <= 256 ? 256 : 512;
   static constexpr int PER_SM = TILES == 2 ? 1 : 2;
+  static constexpr int CHAIN = kChainKeys / BN;        // steps
+  static_assert((CHAIN & (CHAIN - 1)) == 0, "steps are masked");
 };
 
 // x -> 4 tanh(t / 4), t = x * to_t: t is four times the logit over its cap. The error
@@ -70,7 +73,8 @@ template <int D, int TILES> struct PrefillShape {
 // one of the last two, value by value the same whatever hidden columns hold; rows
 // that are not `live` have no say.
 constexpr float kSmallCap = 64.f;
-template <int N> __device__ __forceinline__ void four_tanh(float (&x)[N], float to_t, bool small, bool live, bool edge) {
+template <int N>
+__device__ __forceinline__ void four_tanh(float (&x)[N], float to_t, bool small, bool live, bool edge) {
   float most = 0.f;
 #pragma unroll
   for (int c = 0; c < N; c += 2) {
@@ -125,6 +129,56 @@ template <int N> __device__ __forceinline__ void four_tanh(float (&x)[N], float 
       x[c + 1] = n.y;
     }
   }
+}
+
+// A warp's sums of finished chains, O of its rows in terms of the maximum was[row],
+// kept in the workspace while a new chain runs: rows of D floats, G heads of a token
+// side by side, hq rows from token to token, the first of the tile at kept. Adds
+// what is kept (`add`) to O and leaves the sum there (`back`) or in O's stead in the
+// workspace. Where all 32 rows are live, eight rows' pieces of 32 columns change
+// places, so that a warp touches whole lines. Not inlined: it would cost the loop
+// around it registers.
+template <int D>
+__device__ __noinline__ void chain_sums(uint32_t o_col, float* kept, float* kept_m, int hq, int G, int row, float m,
+                                        bool live, bool add, bool back) {
+  const int shift = __ffs(G) - 1;
+  const bool full = __all_sync(FULL, live);
+  const float was = add && live ? *kept_m : -INFINITY, f = was == -INFINITY ? 0.f : ex2(was - m);
+  auto piece = [&](int c, int e) {
+    const int r = full ? (row & ~7) + e : row, i = full ? row & 7 : e;
+    return reinterpret_cast<float4*>(kept + ((size_t)(r >> shift) * hq + (r & (G - 1))) * D + c * 32) + i;
+  };
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tmem_ld32(o_col + c * 32, o);
+    tmem_wait_ld();
+    tmem_loaded(o);
+    if (add && live) {
+      float4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = *piece(c, e);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o[4 * e] = __float_as_uint(fmaf(f, v[e].x, __uint_as_float(o[4 * e])));
+        o[4 * e + 1] = __float_as_uint(fmaf(f, v[e].y, __uint_as_float(o[4 * e + 1])));
+        o[4 * e + 2] = __float_as_uint(fmaf(f, v[e].z, __uint_as_float(o[4 * e + 2])));
+        o[4 * e + 3] = __float_as_uint(fmaf(f, v[e].w, __uint_as_float(o[4 * e + 3])));
+      }
+    }
+    __syncwarp();
+    if (back) {
+      tmem_st32(o_col + c * 32, o);
+    } else if (live) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        *piece(c, e) = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                   __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+    }
+    __syncwarp();
+  }
+  if (back) tmem_wait_st();
+  else if (live) *kept_m = m;
 }
 
 template <int D, int TILES, bool CAP, bool ALIBI>
@@ -322,6 +376,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       constexpr uint32_t ID_S = mma_idesc(128, BN, false), ID_O = mma_idesc(128, D, true);
       const uint64_t q_d = smem_desc(q_s, 16, 1024), k_d = smem_desc(ring, 16, 1024);
       const uint64_t v_d = smem_desc(ring, BN * 128, 1024);
+      const int chain = p.chained ? P::CHAIN - 1 : -1;
       auto active = [&](int t, int n) { return t == 0 ? n >= a0 && n < b0 : n >= a1 && n < b1; };
       auto issue_s = [&](int t, int buf, int stage) {
         const uint64_t qd = q_d + t * (P::Q_TILE >> 4), kd = k_d + stage * (P::BLOCK >> 4);
@@ -373,7 +428,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
             const int bit = t * SBUF + buf;
             if (!(go = wait(&p_full[t][buf], p_phase >> bit & 1))) break;
             p_phase ^= 1u << bit;
-            issue_o(t, buf, vs, n > (t == 0 ? a0 : a1));
+            issue_o(t, buf, vs, ((n - (t == 0 ? a0 : a1)) & chain) != 0);   // a new chain: O = P V
             if (SBUF == 2) mma_commit(lead, &pv_done[t]);
             if (n + 1 == (t == 0 ? b0 : b1)) mma_commit(lead, &o_full[t]);
           }
@@ -421,104 +476,121 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
     bool ok = true;
     const int first = tile == 0 ? t0[0] : t0[TILES - 1], last = tile == 0 ? t1[0] : t1[TILES - 1];
     const uint32_t o_col = tmem + lanes + P::O_COL + tile * D;
-    for (int i = first; i < last; ++i) {
-      const int buf = SBUF == 2 ? i & 1 : 0, n = n1 - 1 - i;
-      const uint32_t s_col = tmem + lanes + (tile * SBUF + buf) * BN;
-      unsigned bad = 0;
-      if (any_bad) {
-        const int lp = n * pages_per_block + lane;
-        const int page = lane < pages_per_block && lp << page_shift < held ? a.page_indices[e0 + lp] : 0;
-        bad = __ballot_sync(FULL, page < 0 || page >= a.n_phys);
-      }
-      if (!(ok = warp_wait_or_quit(&s_full[tile][buf], s_phase >> buf & 1, p.wait_limit, &s_quit))) break;
-      s_phase ^= 1u << buf;
-      tc_fence_after();
-      uint32_t sv[BN / 32][32];
+    // sums of finished chains: the tile's rows, this row's maximum
+    float* kept = p.part_o + (((size_t)split * a.n_q + row0 + tok0 + tile * tile_tokens) * hq + g * G) * D;
+    float* kept_m = p.part_lse + ((size_t)split * a.n_q + row0 + tok) * hq + h;
+    for (int from = first, to; from < last; from = to) {   // chain by chain
+      to = p.chained ? min(last, from + P::CHAIN) : last;
+      for (int i = from; i < to; ++i) {
+        const int buf = SBUF == 2 ? i & 1 : 0, n = n1 - 1 - i;
+        const uint32_t s_col = tmem + lanes + (tile * SBUF + buf) * BN;
+        unsigned bad = 0;
+        if (any_bad) {
+          const int lp = n * pages_per_block + lane;
+          const int page = lane < pages_per_block && lp << page_shift < held ? a.page_indices[e0 + lp] : 0;
+          bad = __ballot_sync(FULL, page < 0 || page >= a.n_phys);
+        }
+        if (!(ok = warp_wait_or_quit(&s_full[tile][buf], s_phase >> buf & 1, p.wait_limit, &s_quit))) break;
+        s_phase ^= 1u << buf;
+        tc_fence_after();
+        uint32_t sv[BN / 32][32];
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + c * 32, sv[c]);
-      tmem_wait_ld();
+        for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_col + c * 32, sv[c]);
+        tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) tmem_loaded(sv[c]);
-      float x[BN];
+        for (int c = 0; c < BN / 32; ++c) tmem_loaded(sv[c]);
+        float x[BN];
 #pragma unroll
-      for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
-      const int kb = n * BN;
-      const bool edge = __any_sync(FULL, live && (kb < seen.lo || kb + BN > seen.hi || bad));
-      auto hidden = [&](int c) { return kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1); };
-      if (CAP) four_tanh<BN>(x, to_t, a.softcap <= kSmallCap, live, edge);
-      if (ALIBI) {
-        const float d0 = (float)(pos - kb);
+        for (int c = 0; c < BN; ++c) x[c] = __uint_as_float(sv[c / 32][c % 32]);
+        const int kb = n * BN;
+        const bool edge = __any_sync(FULL, live && (kb < seen.lo || kb + BN > seen.hi || bad));
+        auto hidden = [&](int c) { return kb + c < seen.lo || kb + c >= seen.hi || (bad >> (c >> page_shift) & 1); };
+        if (CAP) four_tanh<BN>(x, to_t, a.softcap <= kSmallCap, live, edge);
+        if (ALIBI) {
+          const float d0 = (float)(pos - kb);
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-          x[c] = fmaf(fabsf(d0 - (float)c), -slope2, x[c] * (CAP ? cap2_4 : log2s));
-      }
-      if (edge) {
+          for (int c = 0; c < BN; ++c)
+            x[c] = fmaf(fabsf(d0 - (float)c), -slope2, x[c] * (CAP ? cap2_4 : log2s));
+        }
+        if (edge) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-          if (hidden(c)) x[c] = -INFINITY;
-      }
-      // The maximum lags: with it the block's weights, and only where their sum
-      // passes 2^15 (one above 2^14 is among them, or many above 2^8) or a row
-      // has no maximum yet is a new one taken and the weights done again.
-      float sum;
-      bool again = __any_sync(FULL, m == -INFINITY);
-      for (bool once = false;; once = true) {
-        if (again) {
-          float mc[4] = {x[0], x[1], x[2], x[3]};
+          for (int c = 0; c < BN; ++c)
+            if (hidden(c)) x[c] = -INFINITY;
+        }
+        // The maximum lags: with it the block's weights, and only where their sum
+        // passes 2^15 (one above 2^14 is among them, or many above 2^8) or a row
+        // has no maximum yet is a new one taken and the weights done again.
+        float sum;
+        bool again = __any_sync(FULL, m == -INFINITY);
+        for (bool once = false;; once = true) {
+          if (again) {
+            float mc[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int c = 4; c < BN; c += 4)
+            for (int c = 4; c < BN; c += 4)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mc[e] = fmaxf(mc[e], x[c + e]);
-          const float mx = fmaxf(m, fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * sl2);
-          const float f = mx > m ? ex2(m - mx) : 1.f;   // m = -inf: O and l are zero, f = 0
-          m = mx;
-          l *= f;
-          if (i > first) {
-            // the products up to step i - 1 are in O: with one S buffer the S
-            // that was waited for came after them, with two it came after i - 2
-            if (SBUF == 2 && !(ok = warp_wait_or_quit(&pv_done[tile], (i - 1 - first) & 1, p.wait_limit, &s_quit)))
-              break;
-            tc_fence_after();
+              for (int e = 0; e < 4; ++e) mc[e] = fmaxf(mc[e], x[c + e]);
+            const float mx = fmaxf(m, fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * sl2);
+            const float f = mx > m ? ex2(m - mx) : 1.f;   // m = -inf: O and l are zero, f = 0
+            m = mx;
+            l *= f;
+            if (i > from) {
+              // the products up to step i - 1 are in O: with one S buffer the S
+              // that was waited for came after them, with two it came after i - 2
+              if (SBUF == 2 && !(ok = warp_wait_or_quit(&pv_done[tile], (i - 1 - first) & 1, p.wait_limit, &s_quit)))
+                break;
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_col + c * 32, o);
-              tmem_wait_ld();
-              tmem_loaded(o);
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_col + c * 32, o);
+                tmem_wait_ld();
+                tmem_loaded(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_col + c * 32, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st32(o_col + c * 32, o);
+              }
             }
           }
-        }
-        const float mu = m == -INFINITY ? 0.f : m - 6.f;
-        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 sl = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
+          const float mu = m == -INFINITY ? 0.f : m - 6.f;
+          float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float2 sl = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
 #pragma unroll
-        for (int c = 0; c < BN / 64; ++c) {
-          uint32_t w[32];
+          for (int c = 0; c < BN / 64; ++c) {
+            uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float2 v = make_float2(x[c * 64 + 2 * e], x[c * 64 + 2 * e + 1]);
-            v = fma2(v, sl, nmu);
-            v = make_float2(ex2(v.x), ex2(v.y));
-            sums[e & 1] = add2(sums[e & 1], v);
-            const __half2 hh = __floats2half2_rn(v.x, v.y);
-            w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+            for (int e = 0; e < 32; ++e) {
+              float2 v = make_float2(x[c * 64 + 2 * e], x[c * 64 + 2 * e + 1]);
+              v = fma2(v, sl, nmu);
+              v = make_float2(ex2(v.x), ex2(v.y));
+              sums[e & 1] = add2(sums[e & 1], v);
+              const __half2 hh = __floats2half2_rn(v.x, v.y);
+              w[e] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            tmem_st32(s_col + c * 32, w);
           }
-          tmem_st32(s_col + c * 32, w);
+          sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+          if (once) break;
+          again = __any_sync(FULL, live && sum > 32768.f);
+          if (!again) break;
         }
-        sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-        if (once) break;
-        again = __any_sync(FULL, live && sum > 32768.f);
-        if (!again) break;
+        if (!ok) break;
+        l += sum;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[tile][buf]);
       }
-      if (!ok) break;
-      l += sum;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[tile][buf]);
+      if (!ok || to == last) break;
+      // The chain's sums leave O, which the next step's product begins anew. The next
+      // S being there, the products up to the last step but one are done, and with
+      // one S buffer the last; with two that has its own barrier, whose phase can be
+      // told now.
+      const int buf = SBUF == 2 ? to & 1 : 0;
+      if (!(ok = warp_wait_or_quit(&s_full[tile][buf], s_phase >> buf & 1, p.wait_limit, &s_quit))) break;
+      if (SBUF == 2 && !(ok = warp_wait_or_quit(&pv_done[tile], (to - 1 - first) & 1, p.wait_limit, &s_quit)))
+        break;
+      tc_fence_after();
+      chain_sums<D>(o_col, kept, kept_m, hq, G, row, m, live, from > first, false);
     }
     // A full tile goes through the place of its queries (read by now: the
     // products are done) to one TMA store; another row by row.
@@ -529,11 +601,11 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
       ok = warp_wait_or_quit(&o_full[tile], 0, p.wait_limit, &s_quit);
     if (ok) {
       tc_fence_after();
+      if (p.chained && last - first > P::CHAIN) chain_sums<D>(o_col, kept, kept_m, hq, G, row, m, live, true, true);
       const bool some = live && l > 0.f;               // has a key
       const float inv = some ? 1.f / l : 0.f;
       const float lse2 = some ? m - 6.f + lg2(l) : -INFINITY;
-      const size_t at = ((size_t)row0 + tok) * hq + h;
-      const size_t part = (size_t)split * a.n_q * hq + at;
+      const size_t at = ((size_t)row0 + tok) * hq + h, part = (size_t)split * a.n_q * hq + at;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];

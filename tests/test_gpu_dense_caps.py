@@ -73,7 +73,7 @@ def test_prefill_caps(shape, d):
     case = _case(shape, d, F16, 300 + d)
     cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(case["table"])
     need = qs.prefill_workspace_size(len(lens), sum(rows), table.nnz, h, group, d, 16, F16)
-    assert (need > 16) == cut
+    assert (need > 2 * sum(rows) * h * group * d * 4) == cut     # more than one part of all rows
     q, ind, docs = case["q"].cuda(), dev_i32(case["q_indptr"]), dev_i32(case["at"])
     every = np.arange(sum(rows))
     for cap in CAPS:
@@ -128,7 +128,7 @@ def test_prefill_caps_of_whole_blocks(L, rows, group, cut, d, alibi):
     case["q"] = (torch.sign(case["q"].float()) * torch.sign(key.float()) * torch.sign(torch.rand((rows, group, 1), generator=g) - 0.3)
                  * torch.rand(case["q"].shape, generator=g) * 2.0 ** (size[..., None] - 3)).half()
     cache, table = gpu_cache(case["k_pool"], case["v_pool"], case["summary"]), gpu_table(case["table"])
-    assert (qs.prefill_workspace_size(1, rows, table.nnz, 1, group, d, 16, F16) > 16) == cut
+    assert (qs.prefill_workspace_size(1, rows, table.nnz, 1, group, d, 16, F16) > 2 * rows * group * d * 4) == cut
     slopes = (2.0 ** -np.arange(1, group + 1)).astype(np.float32)
     far = np.abs(np.arange(L - rows, L)[:, None] - np.arange(L)[None])
     bias = np.stack([np.log(np.exp(-float(s) * far).sum(1)) for s in slopes], 1) if alibi else np.log(L)
