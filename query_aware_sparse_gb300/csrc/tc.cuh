@@ -153,21 +153,9 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
-// A wait of one thread: false when `limit` tries (up to about 1 us each) pass,
-// or another role of the CTA has given up; sets the flag then. The first tries
-// do not sleep.
-__device__ __forceinline__ bool wait_or_quit(uint64_t* bar, uint32_t parity, uint32_t limit,
-                                             volatile int* quit) {
-  for (int i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  for (uint32_t i = 0; i < limit; ++i) {
-    if (mbar_try_wait_sleep(bar, parity, 1000u)) return true;
-    if (*quit) return false;
-  }
-  *quit = 1;
-  return false;
-}
-// The same for a whole warp, which agrees on the outcome.
+// A wait of a whole warp, which agrees on the outcome: false when `limit` tries (up
+// to about 1 us each) pass, or another role of the CTA has given up; sets the flag
+// then. The first tries do not sleep.
 __device__ __forceinline__ bool warp_wait_or_quit(uint64_t* bar, uint32_t parity, uint32_t limit,
                                                   volatile int* quit) {
   for (int i = 0; i < 64; ++i)
