@@ -504,8 +504,8 @@ QUEST_API size_t quest_dense_decode_workspace_size(int32_t batch, int32_t nnz, i
  * prefix.
  *   q        : device dtype [n_q, h_kv * group, head_dim]
  *   q_indptr : device int32 [batch + 1], q_indptr[0] = 0
- *   n_q      : host, total rows (>= q_indptr[batch]; rows from there on are not
- *              touched in out and lse)
+ *   n_q      : host, rows of q, out and lse. Rows from q_indptr[batch] on are not
+ *              touched; rows that q_indptr names beyond n_q are left out
  *   mods     : NULL, or as above
  *   out      : device dtype [n_q, h_kv * group, head_dim]
  *   lse      : device fp32 [n_q, h_kv * group], or NULL

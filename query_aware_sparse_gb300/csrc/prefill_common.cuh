@@ -45,7 +45,7 @@ struct PrefillArgs {
 // each: 185 -> 168 us).
 __device__ __forceinline__ bool find_block(const DenseArgs& a, int tokens, int idx, int lane,
                                            int* r_out, int* b_out) {
-  auto rows_of = [&](int r) { return r < a.batch ? a.q_indptr[r + 1] - a.q_indptr[r] : 0; };
+  auto rows_of = [&](int r) { return r < a.batch ? min(a.q_indptr[r + 1], a.n_q) - a.q_indptr[r] : 0; };
   auto blocks_of = [&](int n) { return n > 0 ? (n + tokens - 1) / tokens : 0; };
   // the lane whose request holds block `at` of its own
   auto found = [&](int r0, int at, int cnt) {

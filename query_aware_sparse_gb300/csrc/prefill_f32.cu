@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(256, 1) prefill_f32_kernel(const PrefillArgs p
     const int tok = tok0 + (ty * kR + i) / G;
     pos[i] = len - n_r + tok;
     seen[i] = Seen{0, 0};
-    if (tok < n_r)
+    if (tok < n_r && row0 + tok < a.n_q)
       seen[i] = seen_keys(pos[i], held, a.window, a.doc_starts ? a.doc_starts[row0 + tok] : 0,
                           a.prefix_lens ? a.prefix_lens[r] : 0);
     if (seen[i].hi <= seen[i].lo) seen[i] = Seen{0, 0};

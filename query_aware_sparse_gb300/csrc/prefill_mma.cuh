@@ -215,7 +215,7 @@ prefill_mma_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p
   int t0[TILES], t1[TILES], n0 = 0x7fffffff, n1 = 0;
 #pragma unroll
   for (int t = 0; t < TILES; ++t) {
-    const int ta = tok0 + t * tile_tokens, tb = min(n_r, ta + tile_tokens);
+    const int ta = tok0 + t * tile_tokens, tb = min(min(n_r, a.n_q - row0), ta + tile_tokens);
     int doc = 0x7fffffff;
     if (a.doc_starts) {
       for (int i = ta + lane; i < tb; i += 32) doc = min(doc, a.doc_starts[row0 + i]);
