@@ -61,3 +61,83 @@ def test_prefill_sums(shape, d):
     err = (out.view(-1, d).double() - mean).abs()
     assert (err <= tol).all(), float(((err - 2.0 ** -11) / mean).max())
     assert ((lse.double() - w.sum().log()).abs() <= total + 2.0 ** -22 * 12).all()
+
+
+def _shared(batch, L, rows, h, group, d, S, seed):
+    """Requests of L tokens on the same pages, `rows` query rows each."""
+    from types import SimpleNamespace
+
+    import query_aware_sparse_gb300 as qs
+    pages = -(-L // S)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *shape: torch.randn(shape, generator=g, device="cuda").half()
+    kp, vp, ids = rand(pages, h, S, d), rand(pages, h, S, d), torch.randperm(pages, generator=g, device="cuda")
+    cache = qs.PagedCache(kp, vp, torch.zeros((pages, h, 2, d), dtype=F16, device="cuda"))
+    table = qs.PageTable(dev_i32(np.arange(batch + 1) * pages), ids.to(torch.int32).repeat(batch), dev_i32([L] * batch))
+    q = rand(batch * rows, h * group, d)
+    case = dict(table=SimpleNamespace(seq_lens=np.full(batch, L)), rows=[rows] * batch, group=group, d=d, S=S,
+                q_indptr=np.arange(batch + 1) * rows, gpu=dict(k=kp, v=vp, q=q))
+    return case, cache, table, ids
+
+
+# requests, keys, rows each, KV heads, group, page: one row tile and two, chains of 8192 keys and what is left
+LONG = [(120, 17000, 3, 4, 4, 16), (1, 20000, 9000, 4, 2, 32), (2, 30001, 15000, 2, 4, 16)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", LONG)
+def test_long_rows_under_masks(shape, d):
+    from tests.test_gpu_dense_paths import _row
+    import query_aware_sparse_gb300 as qs
+    batch, L, rows, h, group, S = shape
+    case, cache, table, ids = _shared(*shape[:5], d, S, L + d)
+    at = np.tile(np.arange(L - rows, L), batch)
+    rng = np.random.default_rng(L)
+    slopes = torch.as_tensor(2.0 ** -rng.uniform(8, 14, h * group), dtype=torch.float32, device="cuda")
+    for softcap, window, doc, prefix, bias in ((0.0, 0, None, None, None), (50.0, 16000, None, None, slopes),
+                                               (3.0, 0, at // 7000 * 4000, np.full(batch, 12345), None)):
+        mods = dict(window=window, doc=doc, prefix=prefix, slopes=bias)
+        m = qs.ScoreMods(softcap=softcap, window=window, alibi_slopes=bias,
+                         doc_starts=None if doc is None else dev_i32(doc),
+                         prefix_lens=None if prefix is None else dev_i32(prefix))
+        out, lse = qs.prefill_attn(cache, table, case["gpu"]["q"], group, dev_i32(case["q_indptr"]), mods=m)
+        for r, i in ((0, 0), (batch - 1, rows - 1), (batch // 2, rows // 2), (0, min(rows - 1, 255)), (batch - 1, rows // 3)):
+            o, z, tol_o, tol_l = _row(case, mods, ids, r, i, softcap)
+            e = (out[r * rows + i].double() - o).abs()
+            assert (e <= tol_o).all(), (softcap, r, i, float((e / tol_o).max()))
+            e = (lse[r * rows + i].double() - z).abs()
+            assert (e <= tol_l).all(), (softcap, r, i, float((e / tol_l).max()))
+    assert qs.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", LONG)
+def test_long_rows_repeat_bit_for_bit(shape, d):
+    """Whatever stands in the workspace, on another stream, captured and replayed."""
+    import query_aware_sparse_gb300 as qs
+    batch, L, rows, h, group, S = shape
+    case, cache, table, _ = _shared(*shape[:5], d, S, L + d)
+    q, ind = case["gpu"]["q"], dev_i32(case["q_indptr"])
+    size = qs.prefill_workspace_size(batch, batch * rows, table.nnz, h, group, d, S, F16)
+    space = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    want = qs.prefill_attn(cache, table, q, group, ind, workspace=space)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    same = lambda: torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for fill in (0xff, 0x7b, 0x3c):                    # NaN, large numbers, ordinary ones
+        space.fill_(fill)
+        qs.prefill_attn(cache, table, q, group, ind, out=out, lse=lse, workspace=space)
+        assert same(), fill
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    qs.prefill_attn(cache, table, q, group, ind, out=out, lse=lse, workspace=space, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qs.prefill_attn(cache, table, q, group, ind, out=out, lse=lse, workspace=space)
+    for _ in range(3):
+        out.zero_()
+        space.fill_(0xff)
+        graph.replay()
+        assert same()
+    assert qs.device_error() == 0
