@@ -31,11 +31,14 @@
 // Rows of V that hold no valid token are zeroed in shared memory (0 * NaN of a
 // stale slot would be NaN); such keys' S is replaced, never added to.
 //
-// Measured (d 128): a 16384-token prompt of 32 heads 1410 us, 1560 TFLOP/s (the
-// GPU at its power cap, 1.6 GHz; cuBLAS sustains 1712); in steady state 2560
+// Measured (d 128): a 16384-token prompt of 32 heads 1490 us, 1480 TFLOP/s (the
+// GPU at its power cap, 1.6 to 1.8 GHz; cuBLAS sustains 1712); in steady state 2560
 // cycles for two tiles and 128 keys, of which the products take 2048. 2048 of
-// 65536 tokens, 8 KV heads of 4, capped, 2240 us; 16 requests of four tokens over
-// up to 32768, 171 us, 5370 GB/s.
+// 65536 tokens, 8 KV heads of 4, 1490 us, capped 2160; 16 requests of four tokens
+// over up to 32768, 152 us, 6040 GB/s. d 64: 16384 tokens of 32 heads 1080 us.
+// Against 64 bits outputs are 2.6e-4 off (2-norm): 1.9e-4 by their own rounding to
+// fp16, 1.8e-4 by that of P and the chains. P as two fp16 numbers, as in dense
+// decode, would take three products where there are two.
 #pragma once
 
 #include "prefill_common.cuh"
@@ -69,7 +72,7 @@ template <int D, int TILES> struct PrefillShape {
 //     result, |t| held at 32, where tanh is 1 to 4 units: the small logits of rows
 //     next to ones near a large cap keep their accuracy.
 // R, N and D fitted at Chebyshev nodes. 2048 tokens over 65536 keys, 32 heads, d 128:
-// 2.03, 2.75, 3.00 and 3.58 ms. Blocks where a row's keys begin or end (`edge`) take
+// 2.10, 2.88, 3.12 and 3.65 ms. Blocks where a row's keys begin or end (`edge`) take
 // one of the last two, value by value the same whatever hidden columns hold; rows
 // that are not `live` have no say.
 constexpr float kSmallCap = 64.f;
