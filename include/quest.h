@@ -59,7 +59,8 @@ typedef enum { QUEST_F32 = 0, QUEST_F16 = 1 } quest_dtype;
 #define QUEST_DEVERR_TABLE_RANGE  0x2u  /* append/selection beyond the page table    */
 #define QUEST_DEVERR_EMPTY_PAGE   0x4u  /* selected page holds no valid token        */
 #define QUEST_DEVERR_WAIT_TIMEOUT 0x8u  /* an in-kernel wait hit its iteration limit */
-#define QUEST_DEVERR_FP8_RANGE    0x10u /* a key beyond +-448 under an E4M3 summary  */
+#define QUEST_DEVERR_FP8_RANGE    0x10u /* a key beyond +-448 under an E4M3 summary, or a number
+                                           that an E4M3 cache cannot hold             */
 
 /*
  * One layer's paged cache (Quest page §1.2: the summary has logical shape
@@ -529,6 +530,154 @@ QUEST_API size_t quest_prefill_workspace_size(int32_t batch, int32_t n_q, int32_
                                               int32_t h_kv, int32_t group, int32_t head_dim,
                                               int32_t page_size, int32_t dtype);
 
+/*
+ * Norm of query and key heads of quest_norm_rope_append_kv and
+ * quest_quant_append_kv, before the rotation: y = x * w / sqrt(mean(x^2) + eps)
+ * over the head_dim dims of a head, in fp32, without a rounding between the
+ * norm and the rotation.
+ *   q_weight, k_weight : device fp32, 16-byte aligned, [head_dim], or with
+ *                        *_per_head = 1 [heads, head_dim]; NULL: that side is
+ *                        not normed
+ *   eps                : a normal, finite fp32 number > 0
+ */
+typedef struct quest_qk_norm {
+  const float* q_weight;
+  const float* k_weight;
+  int32_t q_per_head;
+  int32_t k_per_head;
+  float eps;
+} quest_qk_norm;
+
+/*
+ * quest_norm_rope_append_kv — quest_rope_append_kv for models that norm every
+ * query and key head before the rotation: norm, rotation, cache write and
+ * summary fold in one pass over the new tokens.
+ *   norm : not NULL
+ *   rope : NULL for layers without a rotation; q then needs norm->q_weight
+ *   the others, strides, errors and padding as quest_rope_append_kv
+ */
+QUEST_API quest_status quest_norm_rope_append_kv(const quest_cache* cache, const quest_pages* pages,
+                                                 const quest_rope* rope, const quest_qk_norm* norm,
+                                                 const void* q, const void* k_new,
+                                                 const void* v_new, int64_t q_stride,
+                                                 int64_t k_stride, int64_t v_stride, int32_t n_new,
+                                                 int32_t group, const int32_t* append_indptr,
+                                                 const int32_t* seq_lens_before, void* q_out,
+                                                 void* stream);
+
+/*
+ * One layer's paged cache in 8 bits: every stored number is an E4M3 code (the
+ * format of quest_cache.summary_fp8) times a power of two of its token and KV
+ * head, 2^e with the least e in [-14, 7] that holds the row's largest magnitude
+ * (448 * 2^e). Such a number is always an fp16 number, so this cache stands for
+ * an fp16 cache of those numbers: quest_quant_read_kv gives exactly them, and
+ * the page summaries bound exactly them (the reason to keep the rounding out of
+ * the bound: Quest page §3 eq (15)).
+ *   pool    : device, 16-byte aligned, [n_phys, h_kv, quest_quant_page_bytes]:
+ *             one record per page and KV head,
+ *               K codes  uint8 [head_dim / 64][S][64]
+ *               V codes  uint8 [S / 16][head_dim / 32][8][4][4][2][2]: at
+ *                        [s][i][g][t][c][hi][lo] dim 32 i + 4 g + c of token
+ *                        16 s + 8 hi + 2 t + lo
+ *               K scales uint8 [S], V scales uint8 [S]: 127 + e (E8M0)
+ *             (S = page_size)
+ *   summary : device, [n_phys, h_kv, 2, head_dim], fp16, or E4M3 codes with
+ *             summary_fp8 = 1, as in quest_cache
+ * Page scores: pass quest_score_pages(_per_head) a quest_cache of dtype
+ * QUEST_F16 with this summary and with `pool` as its k_pool and v_pool; scoring
+ * reads the summary alone.
+ */
+typedef struct quest_quant_cache {
+  void* pool;
+  void* summary;
+  int32_t n_phys;
+  int32_t h_kv;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t summary_fp8;
+} quest_quant_cache;
+
+/* Bytes of one page of one KV head, 2 * page_size * (head_dim + 1); 0 for
+ * unsupported sizes. */
+QUEST_API size_t quest_quant_page_bytes(int32_t page_size, int32_t head_dim);
+
+/*
+ * quest_quant_append_kv — the append into a quest_quant_cache: keys are normed
+ * (norm, may be NULL) and rotated (rope, may be NULL: with neither they come as
+ * they are to be kept) and rounded to fp16 as quest_norm_rope_append_kv does,
+ * then quantised; values are quantised; the keys as stored are folded into the
+ * page summaries as quest_append_kv does with its keys.
+ *   q, k_new, v_new, q_out : device fp16; q needs rope or norm->q_weight
+ *   the others as quest_norm_rope_append_kv
+ * A magnitude above 448 * 2^7 = 57344 is kept as that, what is not a number as
+ * 0, and QUEST_DEVERR_FP8_RANGE is set (as for a key beyond the range of an
+ * E4M3 summary).
+ */
+QUEST_API quest_status quest_quant_append_kv(const quest_quant_cache* cache,
+                                             const quest_pages* pages, const quest_rope* rope,
+                                             const quest_qk_norm* norm, const void* q,
+                                             const void* k_new, const void* v_new,
+                                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                             int32_t n_new, int32_t group,
+                                             const int32_t* append_indptr,
+                                             const int32_t* seq_lens_before, void* q_out,
+                                             void* stream);
+
+/*
+ * quest_quant_read_kv — the numbers that a quest_quant_cache holds, as fp16
+ * pages of another pool: for quest_prefill_attn over a cache kept in 8 bits, or
+ * any other call that takes a quest_cache. Table entry e of a request goes to
+ * page dst_indices[e]; the tokens below seq_lens[r] are written, nothing else.
+ *   k_out, v_out : device fp16 [n_dst, h_kv, page_size, head_dim], 16-byte
+ *                  aligned
+ *   dst_indices  : device int32 [nnz], distinct, or NULL: entry e goes to page e
+ * A page outside either pool is skipped (QUEST_DEVERR_PAGE_RANGE), a request's
+ * tokens beyond its page table too (QUEST_DEVERR_TABLE_RANGE). nnz * h_kv <
+ * 2^34, else QUEST_ERR_UNSUPPORTED.
+ */
+QUEST_API quest_status quest_quant_read_kv(const quest_quant_cache* cache,
+                                           const quest_pages* pages, void* k_out, void* v_out,
+                                           int32_t n_dst, const int32_t* dst_indices,
+                                           void* stream);
+
+/*
+ * quest_quant_sparse_decode_attn — quest_sparse_decode_attn over a
+ * quest_quant_cache: the same lists, results and errors, fp32 accuracy against
+ * the stored numbers. The slots of all lists are cut into equal runs, one per
+ * warp; the parts of a list that is cut over several runs are joined by
+ * log-sum-exp in a second kernel, always in the same order.
+ *   q         : device fp16 [batch, h_kv * group, head_dim]
+ *   out       : device fp32, 16-byte aligned
+ *   workspace : device, >= quest_quant_decode_workspace_size(...) bytes, 16-B
+ *               aligned; nothing in it has to be set or kept. Calls that share
+ *               a workspace must not overlap on the GPU.
+ * At most 524288 requests and 2^31 - 1 rows of q, else QUEST_ERR_UNSUPPORTED.
+ */
+QUEST_API quest_status quest_quant_sparse_decode_attn(const quest_quant_cache* cache,
+                                                      const quest_pages* pages, const void* q,
+                                                      int32_t group, const int32_t* sel_logical,
+                                                      const int32_t* sel_phys, int32_t k,
+                                                      float* out, float* lse, float sm_scale,
+                                                      void* workspace, size_t workspace_bytes,
+                                                      void* stream);
+
+/*
+ * quest_quant_dense_decode_attn — quest_dense_decode_attn over a
+ * quest_quant_cache: the same visible keys, mods and errors, q and workspace as
+ * quest_quant_sparse_decode_attn.
+ */
+QUEST_API quest_status quest_quant_dense_decode_attn(const quest_quant_cache* cache,
+                                                     const quest_pages* pages, const void* q,
+                                                     int32_t group, const quest_score_mods* mods,
+                                                     float* out, float* lse, float sm_scale,
+                                                     void* workspace, size_t workspace_bytes,
+                                                     void* stream);
+
+/* Workspace bytes the two calls above need for these sizes on the current
+ * device (0 for unsupported shapes). */
+QUEST_API size_t quest_quant_decode_workspace_size(int32_t batch, int32_t h_kv, int32_t group,
+                                                   int32_t head_dim, int32_t page_size);
+
 /* Phase trace of quest_decode_step (profiling aid, off by default): with a
  * device buffer of at least 16 * max_ctas uint64 set, each later call whose
  * grid has at most max_ctas CTAs writes, per CTA, 16 %globaltimer stamps (ns;
@@ -555,8 +704,8 @@ QUEST_API int32_t quest_set_trace(void* device_buffer, int32_t max_ctas, int32_t
  * waits on a barrier nothing arrives on. mode 2: in later
  * quest_sparse_decode_attn(_noalloc) and quest_union_decode_attn calls, the
  * first copy slot of warp 0 of the first CTA expects 16 bytes more than its
- * copies bring; in later quest_dense_decode_attn and (fp16)
- * quest_prefill_attn calls likewise, and there every wait of that CTA gives
+ * copies bring; in later quest_dense_decode_attn, quest_quant_*_decode_attn and
+ * (fp16) quest_prefill_attn calls likewise, and there every wait of that CTA gives
  * up. Either way that wait runs out: the kernel sets
  * QUEST_DEVERR_WAIT_TIMEOUT, issues no further copies, waits (bounded) for
  * those in flight and returns, its outputs unspecified; the device stays

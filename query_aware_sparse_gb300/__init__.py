@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(_PKG, "libquest.so")
 QUEST_F32, QUEST_F16 = 0, 1
 DEVERR = {1: "page id outside the pool", 2: "beyond the page table",
           4: "selected page holds no valid token", 8: "in-kernel wait timed out",
-          16: "key beyond +-448 under an E4M3 summary"}
+          16: "key beyond +-448 under an E4M3 summary, or a number that an E4M3 cache cannot hold"}
 
 
 class QuestCache(ctypes.Structure):
@@ -49,6 +49,19 @@ class QuestScoreMods(ctypes.Structure):
     _fields_ = [("alibi_slopes", ctypes.c_void_p), ("doc_starts", ctypes.c_void_p),
                 ("prefix_lens", ctypes.c_void_p), ("softcap", ctypes.c_float),
                 ("window", ctypes.c_int32)]
+
+
+class QuestQKNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("q_per_head", ctypes.c_int32), ("k_per_head", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class QuestQuantCache(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("summary", ctypes.c_void_p),
+                ("n_phys", ctypes.c_int32), ("h_kv", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("summary_fp8", ctypes.c_int32)]
 
 
 _lib = None
@@ -103,6 +116,20 @@ def lib() -> ctypes.CDLL:
         L.quest_prefill_attn.restype = I32
         L.quest_prefill_workspace_size.argtypes = [I32, I32, I32, I32, I32, I32, I32, I32]
         L.quest_prefill_workspace_size.restype = SZ
+        append = [P, P, P, P, P, P, P, I64, I64, I64, I32, I32, P, P, P, P]
+        L.quest_norm_rope_append_kv.argtypes = L.quest_quant_append_kv.argtypes = append
+        L.quest_norm_rope_append_kv.restype = L.quest_quant_append_kv.restype = I32
+        L.quest_quant_page_bytes.argtypes = [I32, I32]
+        L.quest_quant_page_bytes.restype = SZ
+        L.quest_quant_read_kv.argtypes = [P, P, P, P, I32, P, P]
+        L.quest_quant_read_kv.restype = I32
+        L.quest_quant_sparse_decode_attn.argtypes = [P, P, P, I32, P, P, I32, P, P, ctypes.c_float,
+                                                     P, SZ, P]
+        L.quest_quant_sparse_decode_attn.restype = I32
+        L.quest_quant_dense_decode_attn.argtypes = [P, P, P, I32, P, P, P, ctypes.c_float, P, SZ, P]
+        L.quest_quant_dense_decode_attn.restype = I32
+        L.quest_quant_decode_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+        L.quest_quant_decode_workspace_size.restype = SZ
         L.quest_set_trace.argtypes = [P, I32, I32, I32, I32, I32, I32, I32, I32]
         L.quest_set_trace.restype = I32
         L.quest_test_step_fault.argtypes = [I32, I32]
@@ -126,7 +153,10 @@ EXPORTED = ("quest_append_kv", "quest_score_pages", "quest_score_pages_per_head"
             "quest_recall_diagnostics", "quest_diag_workspace_size",
             "quest_rope_append_kv", "quest_dense_decode_attn",
             "quest_dense_decode_workspace_size", "quest_prefill_attn",
-            "quest_prefill_workspace_size", "quest_set_trace",
+            "quest_prefill_workspace_size", "quest_norm_rope_append_kv",
+            "quest_quant_page_bytes", "quest_quant_append_kv", "quest_quant_read_kv",
+            "quest_quant_sparse_decode_attn", "quest_quant_dense_decode_attn",
+            "quest_quant_decode_workspace_size", "quest_set_trace",
             "quest_test_step_fault", "quest_get_device_error", "quest_status_string")
 
 
@@ -189,6 +219,76 @@ class PagedCache:
         return cls(kp, vp, sm)
 
 
+class QuantCache:
+    """One layer's pool of E4M3 records + summary (caller-owned torch tensors).
+
+    pool: uint8 [n_phys, h_kv, quant_page_bytes(page_size, head_dim)] (the
+    layout is quest_quant_cache's in quest.h; ``k_codes``, ``v_codes``,
+    ``k_scales`` and ``v_scales`` are views of its parts); summary:
+    [n_phys, h_kv, 2, head_dim], fp16 or, as torch.uint8, E4M3 codes. It goes
+    to the quant_* calls and, for its summary, to the page scores; the calls
+    that read fp16 or fp32 pages take the PagedCache of quant_read_kv.
+    """
+
+    dtype = torch.float16
+
+    def __init__(self, pool, summary, page_size: int, head_dim: int):
+        self.pool, self.summary = pool, summary
+        n_phys, h_kv, _ = pool.shape
+        self.n_phys, self.h_kv, self.page_size, self.head_dim = n_phys, h_kv, page_size, head_dim
+        self.device_index = _common_device(pool, summary)
+        self.summary_fp8 = summary.dtype == torch.uint8
+        _expect("pool", pool, torch.uint8, (n_phys, h_kv, quant_page_bytes(page_size, head_dim)),
+                pool.get_device())
+        _expect("summary", summary, torch.uint8 if self.summary_fp8 else torch.float16,
+                (n_phys, h_kv, 2, head_dim), pool.get_device())
+        self.quant = QuestQuantCache(pool.data_ptr(), summary.data_ptr(), n_phys, h_kv, page_size,
+                                     head_dim, int(self.summary_fp8))
+        # what scoring takes: it reads the summary alone
+        self.scored = QuestCache(pool.data_ptr(), pool.data_ptr(), summary.data_ptr(), n_phys, h_kv,
+                                 page_size, head_dim, QUEST_F16, int(self.summary_fp8))
+
+    @classmethod
+    def empty(cls, n_phys, h_kv, page_size, head_dim, device="cuda", summary_fp8=False):
+        pool = torch.empty((n_phys, h_kv, quant_page_bytes(page_size, head_dim)), dtype=torch.uint8,
+                           device=device)
+        summary = torch.empty((n_phys, h_kv, 2, head_dim), device=device,
+                              dtype=torch.uint8 if summary_fp8 else torch.float16)
+        return cls(pool, summary, page_size, head_dim)
+
+    @property
+    def c(self):
+        raise TypeError("this call reads fp16 or fp32 pages: take the quant_* call, or a PagedCache "
+                        "filled by quant_read_kv")
+
+    def _part(self, start, size, dtype):
+        return self.pool[..., start:start + size].view(dtype)
+
+    @property
+    def k_codes(self):
+        """[n_phys, h_kv, head_dim / 64, page_size, 64], torch.float8_e4m3fn."""
+        n = self.page_size * self.head_dim
+        return self._part(0, n, torch.float8_e4m3fn).unflatten(-1, (self.head_dim // 64, self.page_size, 64))
+
+    @property
+    def v_codes(self):
+        """[n_phys, h_kv, page_size / 16, head_dim / 32, 8, 4, 4, 2, 2], torch.float8_e4m3fn:
+        dim 32 i + 4 g + c of token 16 s + 8 hi + 2 t + lo at [s, i, g, t, c, hi, lo]."""
+        n = self.page_size * self.head_dim
+        return self._part(n, n, torch.float8_e4m3fn).unflatten(
+            -1, (self.page_size // 16, self.head_dim // 32, 8, 4, 4, 2, 2))
+
+    @property
+    def k_scales(self):
+        """[n_phys, h_kv, page_size], torch.float8_e8m0fnu."""
+        return self._part(2 * self.page_size * self.head_dim, self.page_size, torch.float8_e8m0fnu)
+
+    @property
+    def v_scales(self):
+        """[n_phys, h_kv, page_size], torch.float8_e8m0fnu."""
+        return self._part((2 * self.head_dim + 1) * self.page_size, self.page_size, torch.float8_e8m0fnu)
+
+
 class PageTable:
     """Ragged page table on the device: page_indptr [B+1], page_indices [nnz],
     seq_lens [B] (int32). ``nnz`` is kept on the host."""
@@ -212,23 +312,27 @@ def append_kv(cache: PagedCache, table: PageTable, k_new, v_new, append_indptr,
                                  _stream(stream)))
 
 
-def score_pages(cache: PagedCache, table: PageTable, q, group: int, scores=None,
+def _scored(cache) -> QuestCache:
+    return cache.scored if isinstance(cache, QuantCache) else cache.c
+
+
+def score_pages(cache: PagedCache | QuantCache, table: PageTable, q, group: int, scores=None,
                 stream=None):
     """quest_score_pages: scores [h_kv, nnz] fp32 of every page-table entry."""
     if scores is None:
         scores = torch.empty((cache.h_kv, table.nnz), dtype=torch.float32, device=q.device)
-    _check(lib().quest_score_pages(ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q),
+    _check(lib().quest_score_pages(ctypes.byref(_scored(cache)), ctypes.byref(table.c), _ptr(q),
                                    int(group), _ptr(scores), _stream(stream)))
     return scores
 
 
-def score_pages_per_head(cache: PagedCache, table: PageTable, q, group: int, scores=None,
+def score_pages_per_head(cache: PagedCache | QuantCache, table: PageTable, q, group: int, scores=None,
                          stream=None):
     """quest_score_pages_per_head: scores [h_kv * group, nnz] fp32, one row per
     query head (no group max)."""
     if scores is None:
         scores = torch.empty((cache.h_kv * group, table.nnz), dtype=torch.float32, device=q.device)
-    _check(lib().quest_score_pages_per_head(ctypes.byref(cache.c), ctypes.byref(table.c), _ptr(q),
+    _check(lib().quest_score_pages_per_head(ctypes.byref(_scored(cache)), ctypes.byref(table.c), _ptr(q),
                                             int(group), _ptr(scores), _stream(stream)))
     return scores
 
@@ -407,11 +511,11 @@ def _expect_rows(name, t, dtype, shape, device) -> int:
                      f"rows, not {t.dtype} {tuple(t.shape)} on {t.device} with strides {t.stride()}")
 
 
-def _current(cache: PagedCache, table: PageTable) -> int:
+def _current(cache: PagedCache | QuantCache, table: PageTable) -> int:
     """Index of the current device, which has to hold the cache and its page table."""
     dev = cache.device_index
     if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError(f"the cache must be on the current CUDA device, not {cache.k_pool.device}")
+        raise ValueError(f"the cache must be on the current CUDA device, not {cache.summary.device}")
     if table.device_index != dev:
         raise ValueError(f"the page table must be on CUDA device {dev}, not {table.seq_lens.device}")
     return dev
@@ -483,6 +587,162 @@ def rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_
         _ptr(v_new), q_stride, k_stride, v_stride, n, int(group), _ptr(append_indptr),
         _ptr(seq_lens_before), _ptr(q_out), _raw_stream(stream, dev)))
     return q_out
+
+
+class QKNorm:
+    """quest_qk_norm: device fp32 weights [d], or [heads, d] for one per head
+    (either may be None: that side is not normed), kept alive here."""
+
+    def __init__(self, q_weight, k_weight, eps: float = 1e-6):
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+        per_head = [int(w is not None and w.dim() == 2) for w in (q_weight, k_weight)]
+        self.c = QuestQKNorm(_ptr(q_weight), _ptr(k_weight), *per_head, self.eps)
+
+    def check(self, h_q, h_kv, d, device):
+        for name, w, heads in (("q_weight", self.q_weight, h_q), ("k_weight", self.k_weight, h_kv)):
+            if w is not None:
+                _expect(name, w, torch.float32, (heads, d) if w.dim() == 2 else (d,), device)
+
+
+def _append_args(cache, table, q, k_new, v_new, append_indptr, seq_lens_before, inv_freq, group,
+                 q_out, positions, interleaved, stream, dev):
+    """Checks what the normed and the E4M3 append share: (QuestRope or None,
+    q_out, the arguments of the C calls from q on)."""
+    dt, n = cache.dtype, k_new.shape[0]
+    h, d = cache.h_kv, cache.head_dim
+    kv = (n, h, d)
+    k_stride = _expect_rows("k_new", k_new, dt, kv, dev)
+    v_stride = _expect_rows("v_new", v_new, dt, kv, dev)
+    _expect("append_indptr", append_indptr, torch.int32, (table.batch + 1,), dev)
+    _expect("seq_lens_before", seq_lens_before, torch.int32, (table.batch,), dev)
+    rope = None
+    if inv_freq is not None:
+        _expect("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
+        if positions is not None:
+            _expect("positions", positions, torch.int32, (n,), dev)
+        rope = QuestRope(_ptr(inv_freq), _ptr(positions), 2 * inv_freq.numel(), int(bool(interleaved)))
+    elif positions is not None:
+        raise ValueError("positions need inv_freq")
+    q_stride = 0
+    if q is not None:
+        rows = (n, h * group, d)
+        q_stride = _expect_rows("q", q, dt, rows, dev)
+        if q_out is None:
+            q_out = _result(rows, dt, dev, stream)
+        _expect("q_out", q_out, dt, rows, dev)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    return rope, q_out, (_ptr(q), _ptr(k_new), _ptr(v_new), q_stride, k_stride, v_stride, n, int(group),
+                         _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out), _raw_stream(stream, dev))
+
+
+def norm_rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_indptr,
+                        seq_lens_before, norm: QKNorm, group: int, inv_freq=None, q_out=None,
+                        positions=None, interleaved: bool = False, stream=None):
+    """quest_norm_rope_append_kv: rope_append_kv with every query and key head
+    normed before the rotation, in the same pass; inv_freq None: no rotation.
+    Returns the queries (or None)."""
+    dev = _current(cache, table)
+    norm.check(cache.h_kv * group, cache.h_kv, cache.head_dim, dev)
+    rope, q_out, tail = _append_args(cache, table, q, k_new, v_new, append_indptr, seq_lens_before,
+                                     inv_freq, group, q_out, positions, interleaved, stream, dev)
+    _check(lib().quest_norm_rope_append_kv(
+        ctypes.byref(cache.c), ctypes.byref(table.c), None if rope is None else ctypes.byref(rope),
+        ctypes.byref(norm.c), *tail))
+    return q_out
+
+
+def quant_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page of one KV head in a QuantCache (0: unsupported sizes)."""
+    return int(lib().quest_quant_page_bytes(page_size, head_dim))
+
+
+def quant_append_kv(cache: QuantCache, table: PageTable, q, k_new, v_new, append_indptr,
+                    seq_lens_before, group: int, inv_freq=None, norm: QKNorm | None = None,
+                    q_out=None, positions=None, interleaved: bool = False, stream=None):
+    """quest_quant_append_kv: k_new and v_new [n_new, h_kv, d] (fp16) into the
+    records and the page summaries; keys and queries normed (norm) and rotated
+    (inv_freq) on the way, as in norm_rope_append_kv. With neither, q has to be
+    None. Returns the queries (or None)."""
+    dev = _current(cache, table)
+    if norm is not None:
+        norm.check(cache.h_kv * group, cache.h_kv, cache.head_dim, dev)
+    rope, q_out, tail = _append_args(cache, table, q, k_new, v_new, append_indptr, seq_lens_before,
+                                     inv_freq, group, q_out, positions, interleaved, stream, dev)
+    _check(lib().quest_quant_append_kv(
+        ctypes.byref(cache.quant), ctypes.byref(table.c), None if rope is None else ctypes.byref(rope),
+        None if norm is None else ctypes.byref(norm.c), *tail))
+    return q_out
+
+
+def quant_read_kv(cache: QuantCache, table: PageTable, dst: PagedCache, dst_indices=None,
+                  stream=None) -> None:
+    """quest_quant_read_kv: the numbers that the cache holds into dst's pages:
+    table entry e to page dst_indices[e] (int32 [nnz]; None: page e). dst's
+    summary is left as it is."""
+    dev = _current(cache, table)
+    if (dst.dtype is not torch.float16 or dst.device_index != dev or
+            (dst.h_kv, dst.page_size, dst.head_dim) != (cache.h_kv, cache.page_size, cache.head_dim)):
+        raise ValueError(f"dst must be a fp16 PagedCache of {cache.h_kv} heads, pages of {cache.page_size} "
+                         f"and {cache.head_dim} dims on CUDA device {dev}")
+    if dst_indices is not None:
+        _expect("dst_indices", dst_indices, torch.int32, (table.nnz,), dev)
+    _check(lib().quest_quant_read_kv(
+        ctypes.byref(cache.quant), ctypes.byref(table.c), _ptr(dst.k_pool), _ptr(dst.v_pool), dst.n_phys,
+        _ptr(dst_indices), _raw_stream(stream, dev)))
+
+
+def quant_decode_workspace_size(batch, h_kv, group, head_dim, page_size) -> int:
+    return int(lib().quest_quant_decode_workspace_size(batch, h_kv, group, head_dim, page_size))
+
+
+def _quant_decode_args(cache, table, q, group, out, lse, workspace, stream, dev):
+    B, h_q, d = table.batch, cache.h_kv * group, cache.head_dim
+    _expect("q", q, torch.float16, (B, h_q, d), dev)
+    if out is None:
+        out = _result((B, h_q, d), torch.float32, dev, stream)
+    if lse is None:
+        lse = _result((B, h_q), torch.float32, dev, stream)
+    _expect("out", out, torch.float32, (B, h_q, d), dev)
+    _expect("lse", lse, torch.float32, (B, h_q), dev)
+    if workspace is None:
+        workspace = _scratch(quant_decode_workspace_size(B, cache.h_kv, group, d, cache.page_size), dev, stream)
+    _expect_workspace(workspace, dev)
+    return out, lse, workspace
+
+
+def quant_sparse_decode_attn(cache: QuantCache, table: PageTable, q, group: int, sel_logical, sel_phys,
+                             k: int, out=None, lse=None, sm_scale: float = 0.0, workspace=None,
+                             stream=None):
+    """quest_quant_sparse_decode_attn: (out [B, h_q, d] fp32, lse [B, h_q] fp32)
+    over the pages that select_topk chose (int32 [B, h_kv, k]). ``workspace``:
+    uint8, quant_decode_workspace_size bytes."""
+    dev = _current(cache, table)
+    for name, sel in (("sel_logical", sel_logical), ("sel_phys", sel_phys)):
+        _expect(name, sel, torch.int32, (table.batch, cache.h_kv, k), dev)
+    out, lse, workspace = _quant_decode_args(cache, table, q, group, out, lse, workspace, stream, dev)
+    _check(lib().quest_quant_sparse_decode_attn(
+        ctypes.byref(cache.quant), ctypes.byref(table.c), _ptr(q), int(group), _ptr(sel_logical),
+        _ptr(sel_phys), int(k), _ptr(out), _ptr(lse), float(sm_scale), _ptr(workspace),
+        int(workspace.numel() * workspace.element_size()), _raw_stream(stream, dev)))
+    return out, lse
+
+
+def quant_dense_decode_attn(cache: QuantCache, table: PageTable, q, group: int, out=None, lse=None,
+                            sm_scale: float = 0.0, mods: ScoreMods | None = None, workspace=None,
+                            stream=None):
+    """quest_quant_dense_decode_attn: (out [B, h_q, d] fp32, lse [B, h_q] fp32)
+    of one query per request over all of its cached tokens. ``workspace``: as
+    quant_sparse_decode_attn."""
+    dev = _current(cache, table)
+    if mods is not None:
+        mods.check(cache.h_kv * group, table.batch, table.batch, dev)
+    out, lse, workspace = _quant_decode_args(cache, table, q, group, out, lse, workspace, stream, dev)
+    _check(lib().quest_quant_dense_decode_attn(
+        ctypes.byref(cache.quant), ctypes.byref(table.c), _ptr(q), int(group),
+        None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
+        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _raw_stream(stream, dev)))
+    return out, lse
 
 
 class ScoreMods:

@@ -25,16 +25,20 @@ SOURCES = ["quest_api.cu", "append.cu", "score.cu", "select.cu", "attn.cu", "ste
            "cstep_e4m3_d64.cu", "cstep_e4m3_d128.cu",
            "dense_api.cu", "rope_append.cu", "dense_decode.cu", "prefill.cu",
            "prefill_f16_d64_t1.cu", "prefill_f16_d64_t2.cu", "prefill_f16_d128_t1.cu",
-           "prefill_f16_d128_t2.cu", "prefill_f32.cu"]
+           "prefill_f16_d128_t2.cu", "prefill_f32.cu",
+           "quant_api.cu", "norm_append.cu", "norm_append_f16.cu", "norm_append_f32.cu",
+           "norm_append_e4m3.cu", "quant_read.cu", "quant_decode.cu"]
 SHARED_HEADERS = ("common.cuh", "internal.h")
 STEP_HEADERS = ("topk.cuh", "attn_dev.cuh", "attn_mma.cuh", "step_impl.cuh", "cstep_impl.cuh")
 DENSE_HEADERS = ("dense.h", "dense.cuh", "tc.cuh", "tmap.h",
-                 "prefill_common.cuh", "prefill_mma.cuh", "dense_decode.cuh", "attn_mma.cuh")
+                 "prefill_common.cuh", "prefill_mma.cuh", "dense_decode.cuh", "attn_mma.cuh",
+                 "append_parts.cuh", "norm_append.cuh", "e4m3_page.cuh", "quant.h",
+                 "quant_decode.cuh")
 
 
 def headers_of(src):
     """Headers whose change rebuilds a source file."""
-    own = DENSE_HEADERS if src.startswith(("dense", "prefill", "rope")) else STEP_HEADERS
+    own = DENSE_HEADERS if src.startswith(("dense", "prefill", "rope", "norm", "quant")) else STEP_HEADERS
     return [os.path.join(CSRC, h) for h in SHARED_HEADERS + own] + [
         os.path.join(ROOT, "include", "quest.h")]
 

@@ -8,22 +8,11 @@ namespace {
 
 using quest::aligned16;
 using quest::check_cache;
+using quest::check_mods;
 using quest::check_pages;
+using quest::launched;
 using quest::valid_group;
-
-quest_status launched(cudaError_t e) { return e == cudaSuccess ? QUEST_OK : QUEST_ERR_CUDA; }
-
-// A token stride holds its row and keeps every row on a 16-byte boundary.
-bool valid_stride(int64_t stride, int64_t row, int32_t dtype) {
-  return stride >= row && stride % (dtype == QUEST_F16 ? 8 : 4) == 0;
-}
-
-quest_status check_mods(const quest_score_mods* m) {
-  if (!m) return QUEST_OK;
-  if (!(m->softcap == 0.f || m->softcap >= 1e-6f) || isinf(m->softcap) || m->window < 0)
-    return QUEST_ERR_INVALID_ARG;
-  return QUEST_OK;
-}
+using quest::valid_stride;
 
 bool valid_shape(int32_t h_kv, int32_t group, int32_t head_dim, int32_t page_size, int32_t dtype) {
   return h_kv > 0 && valid_group(group) && (head_dim == 64 || head_dim == 128) &&

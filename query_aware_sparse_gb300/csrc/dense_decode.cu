@@ -24,7 +24,7 @@ static_assert(DecodeShape<float, 64>::WARPS == DecodeShape<float, 128>::WARPS, "
 
 template <typename W, int D>
 cudaError_t launch(const DecodeMaps& maps, const DecodeArgs& p, cudaStream_t s) {
-  using Sh = DecodeShape<typename W::T, D>;
+  using Sh = typename W::Shape;
   cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel<W, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
   if (e != cudaSuccess) return e;
@@ -62,6 +62,7 @@ cudaError_t launch_dense_decode(const DenseArgs& a, cudaStream_t s) {
   p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
   p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
   p.n_warps = plan.warps;
+  p.min_run = 4;
   p.wait_limit = wait_limit();
   DecodeMaps maps;
   const int rows = a.dtype == QUEST_F16 ? 16 : 8;

@@ -40,6 +40,11 @@ struct DecodeMaps { CUtensorMap k, v; };
 
 struct DecodeArgs {
   DenseArgs a;
+  // pages listed for each (request, KV head) instead of the page table's:
+  // [batch, h_kv, sel_k] logical and physical page, -1 = no page
+  const int32_t* sel_logical; const int32_t* sel_phys;
+  int32_t sel_k;
+  int32_t min_run;          // tiles of a run, at least
   long long* starts;        // [batch + 1] tiles before each request, all KV heads
   float* part_o;            // [warps + units, G, D]
   float2* part_ml;          // [warps + units, G]
@@ -61,10 +66,10 @@ template <typename T, int D> struct DecodeShape {
   static constexpr uint32_t SMEM = 1024 + WARPS * STAGES * STAGE;
 };
 
-// Tiles per warp: equal runs, of at least four.
-__device__ __forceinline__ long long run_length(long long tiles, int n_warps) {
-  const long long n = (tiles + n_warps - 1) / n_warps;
-  return n < 4 ? 4 : n;
+// Tiles per warp: equal runs.
+__device__ __forceinline__ long long run_length(long long tiles, const DecodeArgs& p) {
+  const long long n = (tiles + p.n_warps - 1) / p.n_warps;
+  return n < p.min_run ? p.min_run : n;
 }
 
 // The tiles of request r that hold a visible key.
@@ -84,6 +89,11 @@ __device__ __forceinline__ Request request_of(const DenseArgs& a, int r, unsigne
   q.tiles = s.hi > s.lo ? (s.hi + TT - 1) / TT - q.tile0 : 0;
   return q;
 }
+// The same where pages are listed: a list's slots are its tiles.
+__device__ __forceinline__ Request listed_request(const DecodeArgs& p, int r) {
+  const int len = max(0, p.a.seq_lens[r]);
+  return Request{len - 1, 0, len, len, 0, 0, p.sel_k};
+}
 
 // Logit -> base 2, with the call's mods (converged warps only).
 struct Logit {
@@ -94,10 +104,22 @@ struct Logit {
   }
 };
 
-// Running state of the group's heads, fp16 keys. Lane: heads 2 t, 2 t + 1
-// (t = lane % 4), dims 16 mt + lane / 4 and + 8.
-template <int D> struct WarpF16 {
-  using T = __half;
+// The boxes of a tile of a pool's page: tokens slot .. slot + TT - 1.
+template <typename Sh>
+__device__ __forceinline__ void copy_boxes(const DecodeMaps& maps, const DenseArgs& a, int id, int g, int slot,
+                                           uint32_t dst, uint64_t* bar, uint64_t pol) {
+  const int y = (id * a.h_kv + g) * a.page_size + slot;
+#pragma unroll
+  for (int b = 0; b < Sh::BOXES; ++b) {
+    tma_2d_hint(dst + b * Sh::BOX, &maps.k, b * Sh::COLS, y, smem_u32(bar), pol);
+    tma_2d_hint(dst + Sh::TILE + b * Sh::BOX, &maps.v, b * Sh::COLS, y, smem_u32(bar), pol);
+  }
+}
+
+// Running state of the group's heads on the fp16 MMA. Lane: heads 2 t, 2 t + 1
+// (t = lane % 4), rows lane / 4 and + 8 of 16 dims each. Which dims those are,
+// and where keys and values come from, is said by what is derived from it.
+template <int D> struct WarpMma {
   static constexpr int KT = D / 16;
   uint32_t qb[KT][2];
   float m[2], l[2], acc[KT][4], sum[KT][4];
@@ -114,14 +136,13 @@ template <int D> struct WarpF16 {
     since = 0;
   }
 
-  __device__ __forceinline__ void begin(const DenseArgs& a, int r, int g, int lane, float*) {
-    const int head = lane >> 2, t = lane & 3;
-    const __half* q = static_cast<const __half*>(a.q) + ((size_t)r * a.h_kv * a.group + g * a.group + head) * D;
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        qb[k][i] = head < a.group ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * t) : 0u;
+  // The row of q that the lane holds a part of (null: a column without a head).
+  __device__ __forceinline__ static const __half* query(const DenseArgs& a, int r, int g, int lane) {
+    const int head = lane >> 2;
+    return head < a.group ? static_cast<const __half*>(a.q) + (((size_t)r * a.h_kv + g) * a.group + head) * D : nullptr;
+  }
+  __device__ __forceinline__ void clear(const DenseArgs& a, int g, int lane) {
+    const int t = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       m[i] = -INFINITY;
@@ -135,36 +156,23 @@ template <int D> struct WarpF16 {
     since = 0;
   }
 
-  // tokens tok0 .. tok0 + 15 of the tile in shared memory at k_s and v_s
-  __device__ __forceinline__ void tile(const DenseArgs& a, const Request& rq, int tok0, uint32_t k_s,
-                                       uint32_t v_s, const float*, float scale2, int lane) {
-    const int r8 = lane & 7, mat = lane >> 3, t = lane & 3;
-    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-      const int row = r8 + 8 * (mat & 1);
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const uint32_t at = k_s + (k >> 2) * 2048 + row * 128 + ((((k & 3) * 2 + (mat >> 1)) ^ r8) << 4);
-        uint32_t a0, a1, a2, a3;
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3) : "r"(at));
-        if (k & 1) mma_f16_16816(s1, a0, a1, a2, a3, qb[k][0], qb[k][1]);
-        else mma_f16_16816(s0, a0, a1, a2, a3, qb[k][0], qb[k][1]);
-      }
-    }
+  // Products s of tokens tok0 .. tok0 + 15 -> their weights, as the two halves
+  // of P^T (k index of a half: 2 t, 2 t + 1 (+ 8)).
+  __device__ __forceinline__ void weigh(const DenseArgs& a, const Request& rq, int tok0, const float (&s)[4],
+                                        float scale2, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
     const int ta = tok0 + (lane >> 2), tb = ta + 8;
     float x[4];
     if (a.softcap > 0.f || a.slopes) {
       const float cap2 = a.softcap * LOG2E, inv = 1.f / cap2;
       const Logit f0{scale2, cap2, inv, slope2[0]}, f1{scale2, cap2, inv, slope2[1]};
       const int da = abs(rq.pos - ta), db = abs(rq.pos - tb);
-      x[0] = f0(s0[0] + s1[0], da);
-      x[1] = f1(s0[1] + s1[1], da);
-      x[2] = f0(s0[2] + s1[2], db);
-      x[3] = f1(s0[3] + s1[3], db);
+      x[0] = f0(s[0], da);
+      x[1] = f1(s[1], da);
+      x[2] = f0(s[2], db);
+      x[3] = f1(s[3], db);
     } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = (s0[c] + s1[c]) * scale2;
+      for (int c = 0; c < 4; ++c) x[c] = s[c] * scale2;
     }
     const bool edge = tok0 < rq.lo || tok0 + 16 > rq.hi;
     if (edge) {
@@ -187,7 +195,6 @@ template <int D> struct WarpF16 {
         }
       }
     }
-    uint32_t hi[2], lo[2];
     const float b0 = m[0] == -INFINITY ? 0.f : m[0] - 6.f, b1 = m[1] == -INFINITY ? 0.f : m[1] - 6.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -200,6 +207,74 @@ template <int D> struct WarpF16 {
       asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(hi[i]) : "r"(*reinterpret_cast<const uint32_t*>(&h)));
       asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(lo[i]) : "r"(*reinterpret_cast<const uint32_t*>(&rest)));
     }
+  }
+
+  // The state as o (times `whole ? 1 / l : 1`), m and l of the lane's heads;
+  // `write` puts sum's column i, times a factor, into o.
+  template <typename F, typename W>
+  __device__ __forceinline__ void finish_heads(const DenseArgs& a, bool whole, int lane, F put, W write) {
+    const int t = lane & 3;
+    settle();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) l[i] += __shfl_xor_sync(FULL, l[i], o);
+      const int head = 2 * t + i;
+      if (head < a.group)
+        write(put(head, m[i], l[i], (lane >> 2) == 0), i, whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f);
+    }
+  }
+};
+
+// fp16 keys and values: dims 16 k + lane / 4 and + 8.
+template <int D> struct WarpF16 : WarpMma<D> {
+  using Base = WarpMma<D>;
+  using Shape = DecodeShape<__half, D>;
+  using Source = DecodeMaps;
+  using Base::KT;
+  using Base::acc;
+  using Base::qb;
+  using Base::since;
+  using Base::sum;
+  static constexpr bool kQueryShared = false;
+
+  __device__ __forceinline__ static void copy(const Source& maps, const DenseArgs& a, int id, int g, int slot,
+                                              uint32_t dst, uint64_t* bar, uint64_t pol) {
+    copy_boxes<Shape>(maps, a, id, g, slot, dst, bar, pol);
+  }
+
+  __device__ __forceinline__ void begin(const DenseArgs& a, int r, int g, int lane, float*) {
+    const int t = lane & 3;
+    const __half* q = Base::query(a, r, g, lane);
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        qb[k][i] = q ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * i + 2 * t) : 0u;
+    Base::clear(a, g, lane);
+  }
+
+  // tokens tok0 .. tok0 + 15 of the tile in shared memory
+  __device__ __forceinline__ void tile(const DenseArgs& a, const Request& rq, int tok0, uint32_t k_s,
+                                       const float*, float scale2, int lane) {
+    const uint32_t v_s = k_s + Shape::TILE;
+    const int r8 = lane & 7, mat = lane >> 3, t = lane & 3;
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const int row = r8 + 8 * (mat & 1);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const uint32_t at = k_s + (k >> 2) * 2048 + row * 128 + ((((k & 3) * 2 + (mat >> 1)) ^ r8) << 4);
+        uint32_t a0, a1, a2, a3;
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(a0), "=r"(a1), "=r"(a2), "=r"(a3) : "r"(at));
+        if (k & 1) mma_f16_16816(s1, a0, a1, a2, a3, qb[k][0], qb[k][1]);
+        else mma_f16_16816(s0, a0, a1, a2, a3, qb[k][0], qb[k][1]);
+      }
+    }
+    const float s[4] = {s0[0] + s1[0], s0[1] + s1[1], s0[2] + s1[2], s0[3] + s1[3]};
+    uint32_t hi[2], lo[2];
+    Base::weigh(a, rq, tok0, s, scale2, lane, hi, lo);
     // values of slots without a token may be anything (0 * NaN is NaN): their
     // halves of V^T are cleared. k index of a half: 2 t, 2 t + 1 (+ 8)
     uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;
@@ -219,29 +294,18 @@ template <int D> struct WarpF16 {
       mma_f16_16816(acc[k], a0, a1, a2, a3, hi[0], hi[1]);
       mma_f16_16816(acc[k], a0, a1, a2, a3, lo[0], lo[1]);
     }
-    if (++since == 8) settle();
+    if (++since == 8) Base::settle();
   }
 
-  // The state as o (times `whole ? 1 / l : 1`), m and l of head i, dims 16 k + ..
   template <typename F>
   __device__ __forceinline__ void finish(const DenseArgs& a, bool whole, int lane, F put) {
-    const int t = lane & 3;
-    settle();
+    Base::finish_heads(a, whole, lane, put, [&](float* o, int i, float f) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) l[i] += __shfl_xor_sync(FULL, l[i], o);
-      const int head = 2 * t + i;
-      if (head < a.group) {
-        const float f = whole ? (l[i] > 0.f ? 1.f / l[i] : 0.f) : 1.f;
-        float* o = put(head, m[i], l[i], (lane >> 2) == 0);
-#pragma unroll
-        for (int k = 0; k < KT; ++k) {
-          o[16 * k + (lane >> 2)] = sum[k][i] * f;
-          o[16 * k + (lane >> 2) + 8] = sum[k][2 + i] * f;
-        }
+      for (int k = 0; k < KT; ++k) {
+        o[16 * k + (lane >> 2)] = sum[k][i] * f;
+        o[16 * k + (lane >> 2) + 8] = sum[k][2 + i] * f;
       }
-    }
+    });
   }
 };
 
@@ -249,10 +313,17 @@ template <int D> struct WarpF16 {
 // four dims (conflict free under the swizzle), q in shared memory; values:
 // D / 32 dims per lane.
 template <int D, int G> struct WarpF32 {
-  using T = float;
+  using Shape = DecodeShape<float, D>;
+  using Source = DecodeMaps;
+  static constexpr bool kQueryShared = true;
   static constexpr int E = D / 32;
   float m[G], l[G], acc[G][E];
   float slope2[G];
+
+  __device__ __forceinline__ static void copy(const Source& maps, const DenseArgs& a, int id, int g, int slot,
+                                              uint32_t dst, uint64_t* bar, uint64_t pol) {
+    copy_boxes<Shape>(maps, a, id, g, slot, dst, bar, pol);
+  }
 
   __device__ __forceinline__ void begin(const DenseArgs& a, int r, int g, int lane, float* qs) {
     const float* q = static_cast<const float*>(a.q) + ((size_t)r * a.h_kv + g) * G * D;
@@ -270,7 +341,8 @@ template <int D, int G> struct WarpF32 {
   }
 
   __device__ __forceinline__ void tile(const DenseArgs& a, const Request& rq, int tok0, uint32_t k_s,
-                                       uint32_t v_s, const float* qs, float scale2, int lane) {
+                                       const float* qs, float scale2, int lane) {
+    const uint32_t v_s = k_s + Shape::TILE;
     const int tok = lane & 7, part = lane >> 3;
     float s[G];
 #pragma unroll
@@ -343,17 +415,17 @@ template <int D, int G> struct WarpF32 {
   }
 };
 
-template <typename W, int D>
-__global__ void __launch_bounds__(DecodeShape<typename W::T, D>::WARPS * 32, 1)
-dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p) {
-  using T = typename W::T;
-  using Sh = DecodeShape<T, D>;
+// LIST: the tiles are the pages that p.sel_* list, else the page table's.
+template <typename W, int D, bool LIST = false>
+__global__ void __launch_bounds__(W::Shape::WARPS * 32, 1)
+dense_decode_kernel(const __grid_constant__ typename W::Source source, const DecodeArgs p) {
+  using Sh = typename W::Shape;
   constexpr int TT = Sh::TT, NST = Sh::STAGES, NW = Sh::WARPS;
-  constexpr bool F32 = sizeof(T) == 4;
+  constexpr bool QS = W::kQueryShared;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t s_bar[NW][NST];
   __shared__ int4 s_meta[NW][NST];
-  __shared__ __align__(16) float s_q[F32 ? NW : 1][F32 ? 8 * D : 1];
+  __shared__ __align__(16) float s_q[QS ? NW : 1][QS ? 8 * D : 1];
   const DenseArgs& a = p.a;
   const int warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int page_shift = a.page_size == 16 ? 4 : 5;
@@ -365,7 +437,8 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   // Tiles of all requests before the run, and the run. A warp looks at 32
   // requests at a time: with no more than that by itself, else the sums of all
   // chunks go through the ring's space, before it is used.
-  const int chunks = (a.batch + 31) / 32;
+  // Lists have as many tiles each as slots, so nothing is looked at.
+  const int chunks = LIST ? 1 : (a.batch + 31) / 32;
   unsigned* err = blockIdx.x == 0 ? a.err : nullptr;
   auto chunk_tiles = [&](int c, unsigned* e) {         // of the lane's request, all KV heads
     const int r = c * 32 + lane;
@@ -381,7 +454,9 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   };
   long long* sums = reinterpret_cast<long long*>(((uintptr_t)smem_raw + 15) & ~(uintptr_t)15);
   long long n = 0, incl = 0, all;                      // of the lane's request of the chunk in hand
-  if (chunks == 1) {
+  if constexpr (LIST) {
+    all = (long long)a.batch * a.h_kv * p.sel_k;
+  } else if (chunks == 1) {
     n = chunk_tiles(0, err);
     incl = running(n);
     all = __shfl_sync(FULL, incl, 31);
@@ -403,13 +478,16 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
     __syncthreads();
     all = sums[chunks];
   }
-  const long long run = run_length(all, p.n_warps);
+  const long long run = run_length(all, p);
   // neighbouring runs on different SMs: few tiles spread over the device
   const int wid = warp * gridDim.x + blockIdx.x;
   const long long first = min(all, wid * run), last = min(all, first + run);
 
   // for the joining kernel: where each request starts (a share per CTA)
-  for (int c = blockIdx.x * NW + warp; c < chunks; c += gridDim.x * NW) {
+  if constexpr (LIST) {
+    for (int i = blockIdx.x * NW * 32 + threadIdx.x; i <= a.batch; i += gridDim.x * NW * 32)
+      p.starts[i] = (long long)i * a.h_kv * p.sel_k;
+  } else for (int c = blockIdx.x * NW + warp; c < chunks; c += gridDim.x * NW) {
     if (chunks > 1) {
       n = chunk_tiles(c, nullptr);
       incl = running(n);
@@ -421,7 +499,13 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   // the run's first request
   int r = 0, g = 0, at = 0;                            // load cursor: request, KV head, tile of it
   Request rq{};
-  if (first < last) {
+  if (LIST && first < last) {
+    const long long unit = first / p.sel_k;
+    r = (int)(unit / a.h_kv);
+    g = (int)(unit % a.h_kv);
+    at = (int)(first % p.sel_k);
+    rq = listed_request(p, r);
+  } else if (first < last) {
     int c = 0;
     long long base = 0;
     if (chunks > 1) {
@@ -455,38 +539,48 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
   const float scale2 = a.scale * LOG2E;
   const uint64_t pol = evict_first_policy();
   int issued = 0;
-  int ids = 0, ids_at = -1, ids_r = -1;                // page ids of 32 tiles, one per lane
+  int ids = 0, ids_at = -1, ids_r = -1, ids_g = 0;     // page ids of 32 tiles, one per lane
+  int pages = 0;                                       // LIST: their logical pages
 
   const bool fault = a.test_fault == 2 && blockIdx.x == 0 && warp == 0;
 
   // Start the copies of the cursor's tile into a place of the ring, and step on.
   auto issue = [&](int st) {
-    if (ids_r != r || at < ids_at || at >= ids_at + 32) {
+    if (ids_r != r || (LIST && ids_g != g) || at < ids_at || at >= ids_at + 32) {
       ids_r = r;
+      ids_g = g;
       ids_at = at;
-      ids = at + lane < rq.tiles ? a.page_indices[rq.e0 + ((rq.tile0 + at + lane) * TT >> page_shift)] : 0;
+      if constexpr (LIST) {
+        const size_t i = ((size_t)r * a.h_kv + g) * p.sel_k + at + lane;
+        pages = at + lane < p.sel_k ? p.sel_logical[i] : -1;
+        ids = pages >= 0 ? p.sel_phys[i] : -1;
+        if (pages >= (rq.held + TT - 1) / TT) {        // no token of the request
+          report(a.err, QUEST_DEVERR_EMPTY_PAGE);
+          pages = -1;
+        }
+      } else {
+        ids = at + lane < rq.tiles ? a.page_indices[rq.e0 + ((rq.tile0 + at + lane) * TT >> page_shift)] : 0;
+      }
     }
     const int id = __shfl_sync(FULL, ids, at - ids_at);
-    const bool bad = id < 0 || id >= a.n_phys;
+    const int lp = LIST ? __shfl_sync(FULL, pages, at - ids_at) : rq.tile0 + at;
+    const bool none = LIST && lp < 0, bad = none || id < 0 || id >= a.n_phys;
     if (lane == 0) {
-      s_meta[warp][st] = make_int4(r, g, at, bad);
+      s_meta[warp][st] = make_int4(r, g, at, bad ? -1 : lp * TT);
       if (!bad) {
         uint64_t* bar = &s_bar[warp][st];
         mbar_expect_tx(bar, Sh::STAGE + (fault && st == 0 ? 16 : 0));
-        const int y = ((id * a.h_kv + g) << page_shift) + ((rq.tile0 + at) * TT & (a.page_size - 1));
-        const uint32_t dst = ring + st * Sh::STAGE;
-#pragma unroll
-        for (int b = 0; b < Sh::BOXES; ++b) {
-          tma_2d_hint(dst + b * Sh::BOX, &maps.k, b * Sh::COLS, y, smem_u32(bar), pol);
-          tma_2d_hint(dst + Sh::TILE + b * Sh::BOX, &maps.v, b * Sh::COLS, y, smem_u32(bar), pol);
-        }
-      } else {
+        W::copy(source, a, id, g, lp * TT & (a.page_size - 1), ring + st * Sh::STAGE, bar, pol);
+      } else if (!none) {
         report(a.err, QUEST_DEVERR_PAGE_RANGE);
       }
     }
     if (++issued < total && ++at == rq.tiles) {
       at = 0;
-      if (++g == a.h_kv) {
+      if (++g == a.h_kv && LIST) {
+        g = 0;
+        rq = listed_request(p, ++r);
+      } else if (!LIST && g == a.h_kv) {
         g = 0;
         // the next request with a tile, 32 at a time (there is one: more is to come)
         for (int r0 = r + 1;; r0 += 32) {
@@ -530,17 +624,16 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
     meta = s_meta[warp][st];
     if (meta.x != cr || meta.y != cg) {
       if (cr >= 0) flush(cq.tiles);
-      if (meta.x != cr) cq = request_of<TT>(a, meta.x, nullptr);
+      if (meta.x != cr) cq = LIST ? listed_request(p, meta.x) : request_of<TT>(a, meta.x, nullptr);
       cr = meta.x;
       cg = meta.y;
       c_first = meta.z;
-      w.begin(a, cr, cg, lane, s_q[F32 ? warp : 0]);
+      w.begin(a, cr, cg, lane, s_q[QS ? warp : 0]);
     }
-    if (!meta.w) {
+    if (meta.w >= 0) {
       if (!warp_wait_bounded(&s_bar[warp][st], phase >> st & 1, p.wait_limit)) { ok = false; break; }
       phase ^= 1u << st;
-      const uint32_t at_s = ring + st * Sh::STAGE;
-      w.tile(a, cq, (cq.tile0 + meta.z) * TT, at_s, at_s + Sh::TILE, s_q[F32 ? warp : 0], scale2, lane);
+      w.tile(a, cq, meta.w, ring + st * Sh::STAGE, s_q[QS ? warp : 0], scale2, lane);
     }
     __syncwarp();
     if (done + NST < total) issue(st);
@@ -550,7 +643,7 @@ dense_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs p)
     if (lane == 0) report(a.err, QUEST_DEVERR_WAIT_TIMEOUT);
     for (int k = 0; k < NST && done + k < total; ++k) {
       const int i = (st + k) % NST;
-      if (!s_meta[warp][i].w) warp_wait_bounded(&s_bar[warp][i], phase >> i & 1, p.wait_limit);
+      if (s_meta[warp][i].w >= 0) warp_wait_bounded(&s_bar[warp][i], phase >> i & 1, p.wait_limit);
     }
     return;
   }
@@ -571,7 +664,7 @@ __global__ void __launch_bounds__(kJoinThreads) dense_decode_join_kernel(const D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / a.group, h = blockIdx.x % a.group;
   const int r = unit / a.h_kv, g = unit % a.h_kv;
-  const long long run = run_length(p.starts[a.batch], p.n_warps);
+  const long long run = run_length(p.starts[a.batch], p);
   const long long n = (p.starts[r + 1] - p.starts[r]) / a.h_kv, u0 = p.starts[r] + g * n;
   const size_t row = (size_t)unit * a.group + h;
   float* out = static_cast<float*>(a.out) + row * D;

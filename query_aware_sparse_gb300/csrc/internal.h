@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stddef.h>
 
 #include <atomic>
@@ -36,6 +37,20 @@ inline quest_status check_pages(const quest_pages* p, bool need_seq_lens) {
 }
 
 inline bool valid_group(int32_t g) { return g == 1 || g == 2 || g == 4 || g == 8; }
+
+inline quest_status launched(cudaError_t e) { return e == cudaSuccess ? QUEST_OK : QUEST_ERR_CUDA; }
+
+// A token stride holds its row and keeps every row on a 16-byte boundary.
+inline bool valid_stride(int64_t stride, int64_t row, int32_t dtype) {
+  return stride >= row && stride % (dtype == QUEST_F16 ? 8 : 4) == 0;
+}
+
+inline quest_status check_mods(const quest_score_mods* m) {
+  if (!m) return QUEST_OK;
+  if (!(m->softcap == 0.f || m->softcap >= 1e-6f) || isinf(m->softcap) || m->window < 0)
+    return QUEST_ERR_INVALID_ARG;
+  return QUEST_OK;
+}
 
 // quest_test_step_fault's state: the fault mode (0 none, 1 a wait of the
 // cluster step runs out, 2 a wait of the attention split kernel runs out)

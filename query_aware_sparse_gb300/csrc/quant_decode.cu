@@ -1,0 +1,69 @@
+// Decode attention over the E4M3 cache: plan and launch (quant_decode.cuh).
+#include "quant_decode.cuh"
+#include "internal.h"
+#include "tmap.h"
+
+namespace quest {
+namespace {
+
+struct Plan { int warps; size_t part_o, part_ml, bytes; };
+
+Plan plan_quant(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim) {
+  Plan p;
+  p.warps = sm_count() * (head_dim == 64 ? RecordShape<64, 16>::WARPS : RecordShape<128, 16>::WARPS);
+  const size_t slots = ((size_t)p.warps + (size_t)batch * h_kv) * group;
+  p.part_o = (((size_t)batch + 1) * sizeof(long long) + 255) & ~(size_t)255;
+  p.part_ml = p.part_o + slots * head_dim * sizeof(float);
+  p.bytes = p.part_ml + slots * sizeof(float2);
+  return p;
+}
+
+template <int D, int S, bool LIST>
+cudaError_t launch(const DecodeArgs& p, cudaStream_t s) {
+  using W = WarpE4M3<D, S>;
+  using Sh = typename W::Shape;
+  static_assert(Sh::WARPS == RecordShape<D, 16>::WARPS, "one plan for both page sizes");
+  cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel<W, D, LIST>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM);
+  if (e != cudaSuccess) return e;
+  const PageRecords src{static_cast<const uint8_t*>(p.a.k_pool)};
+  e = launch_pdl(dense_decode_kernel<W, D, LIST>, p.n_warps / Sh::WARPS, Sh::WARPS * 32, Sh::SMEM, s, src, p);
+  if (e != cudaSuccess) return e;
+  // the same shared memory split as the kernel before it
+  e = cudaFuncSetAttribute(dense_decode_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, kJoinThreads, 0, s, p);
+}
+
+template <bool LIST> cudaError_t launch_shape(const DecodeArgs& p, cudaStream_t s) {
+  if (p.a.head_dim == 128)
+    return p.a.page_size == 16 ? launch<128, 16, LIST>(p, s) : launch<128, 32, LIST>(p, s);
+  return p.a.page_size == 16 ? launch<64, 16, LIST>(p, s) : launch<64, 32, LIST>(p, s);
+}
+
+}  // namespace
+
+size_t quant_decode_workspace(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim) {
+  return plan_quant(batch, h_kv, group, head_dim).bytes;
+}
+
+cudaError_t launch_quant_decode(const DenseArgs& a, const int32_t* sel_logical, const int32_t* sel_phys,
+                                int32_t k, cudaStream_t s) {
+  const Plan plan = plan_quant(a.batch, a.h_kv, a.group, a.head_dim);
+  char* ws = static_cast<char*>(a.workspace);
+  DecodeArgs p{};
+  p.a = a;
+  p.sel_logical = sel_logical;
+  p.sel_phys = sel_phys;
+  p.sel_k = k;
+  p.min_run = 4;
+  p.starts = reinterpret_cast<long long*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + plan.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  p.n_warps = plan.warps;
+  p.wait_limit = wait_limit();
+  return sel_logical ? launch_shape<true>(p, s) : launch_shape<false>(p, s);
+}
+
+}  // namespace quest
