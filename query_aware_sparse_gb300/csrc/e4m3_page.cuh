@@ -54,7 +54,29 @@ __device__ __forceinline__ int scale_exponent(uint32_t top) {
 }
 // Largest magnitude bits of two fp16 pairs' halves (not a number: above infinity).
 __device__ __forceinline__ uint32_t max_magnitude(uint32_t m, uint32_t h2) {
-  return __vmaxu2(m, h2 & 0x7fff7fffu);
+  uint32_t r;
+  asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %2;\n\tmax.NaN.f16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(h2));
+  return r;
+}
+// The greatest codes at or below four fp16 numbers (two pairs), as e4m3_floor
+// does it, four at a time: round to nearest, and one code down where that is
+// above the number.
+__device__ __forceinline__ uint32_t e4m3_floor4(uint32_t x01, uint32_t x23, bool& ovf) {
+  const uint32_t least = 0xdf00df00u;                   // -448: nothing is kept below
+  uint32_t y01, y23;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y01) : "r"(x01), "r"(least));
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y23) : "r"(x23), "r"(least));
+  ovf = ovf || y01 != x01 || y23 != x23;
+  const uint32_t c01 = e4m3_codes(y01), c23 = e4m3_codes(y23);
+  const uint32_t d01 = e4m3_pair(c01), d23 = e4m3_pair(c23);
+  auto above = [](const uint32_t& d, const uint32_t& y) {
+    return __hgt2_mask(*reinterpret_cast<const __half2*>(&d), *reinterpret_cast<const __half2*>(&y));
+  };
+  uint32_t c = c01 | c23 << 16;
+  const uint32_t down = __byte_perm(above(d01, y01), above(d23, y23), 0x6420);
+  const uint32_t step = ~((c >> 7 & 0x01010101u) * 0xfeu);      // -1, or +1 below zero
+  c = __vadd4(c, step & down);
+  return c & ~__vcmpeq4(c, 0x80808080u);                // a zero stays +0
 }
 // What cannot be kept as it is: not a number becomes 0, more than 448 * 2^7 becomes that.
 __device__ __forceinline__ uint32_t keepable(uint32_t h2) {

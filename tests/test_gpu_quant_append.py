@@ -56,10 +56,8 @@ def _check(seed, lens, before, *, h=2, group=2, d=128, S=16, fp8=False, rope=Fal
     phys = table.page_indices[table.page_indptr[req] + pos // S]
     if rope or norm:
         plain = qs.PagedCache.empty(table.n_phys, h, S, d, F16)
-        if norm:
-            want_q = qs.norm_rope_append_kv(plain, *args, qk, group, inv_freq=inv, interleaved=interleaved)
-        else:
-            want_q = qs.rope_append_kv(plain, *args, inv, group, interleaved=interleaved)
+        want_q = qs.norm_rope_append_kv(plain, *args, qk or qs.QKNorm(None, None), group, inv_freq=inv,
+                                        interleaved=interleaved)
         qs.device_error()
         assert (q_out is None) == (not with_q) and (not with_q or torch.equal(q_out, want_q))
         keys = np_of(plain.k_pool)[phys, :, pos % S]

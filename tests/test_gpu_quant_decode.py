@@ -281,6 +281,37 @@ def test_two_calls_at_once():
         assert all(torch.equal(x, y) for x, y in zip(want[:4], o[:4]))
 
 
+def test_one_workspace_for_calls_of_all_sizes():
+    """Large and small calls, lists and tables, in any order: what one leaves in
+    the workspace is nothing to the next."""
+    import query_aware_sparse_gb300 as qs
+    rng = np.random.default_rng(8)
+    n = max(qs.quant_decode_workspace_size(300, 3, 8, d, 16) for d in (64, 128))
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (lens, h, G, d, S) in enumerate([([9000, 5], 2, 8, 128, 16), ([40], 1, 1, 64, 32),
+                                            (rng.integers(0, 300, 300).tolist(), 3, 2, 64, 16), ([20000], 1, 8, 64, 16),
+                                            ([7000, 0, 7000], 3, 4, 128, 32)]):
+        case = quant_case(300 + i, lens, h_kv=h, group=G, d=d, S=S)
+        sel, phys = (dev_i32(x) for x in _lists(case, 30, i))
+        c, t, q = gpu_quant(case), gpu_table(case["table"]), case["q"].cuda()
+        calls.append(lambda c=c, t=t, q=q, G=G, **kw: qs.quant_dense_decode_attn(c, t, q, G, **kw))
+        calls.append(lambda c=c, t=t, q=q, G=G, sel=sel, phys=phys, **kw:
+                     qs.quant_sparse_decode_attn(c, t, q, G, sel, phys, 30, **kw))
+    want = [call() for call in calls]
+    for i in rng.integers(0, len(calls), 60):
+        out, lse = calls[i](workspace=ws)
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), i
+    assert qs.device_error() == 0
+
+
+def test_one_long_request_over_all_multiprocessors():
+    """A unit that every CTA has a part of, of 1 to 8 heads."""
+    for G, d in ((1, 128), (8, 128), (2, 64), (8, 64)):
+        _dense(quant_case(310 + G, [40000], h_kv=1, group=G, d=d, S=16))
+    _sparse(quant_case(320, [60000], h_kv=1, group=2, d=64, S=16), 3500)
+
+
 def test_without_lse_and_with_a_scale():
     import ctypes
     import query_aware_sparse_gb300 as qs
