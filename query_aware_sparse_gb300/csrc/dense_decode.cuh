@@ -552,8 +552,9 @@ dense_decode_kernel(const __grid_constant__ typename W::Source source, const Dec
       ids_at = at;
       if constexpr (LIST) {
         const size_t i = ((size_t)r * a.h_kv + g) * p.sel_k + at + lane;
-        pages = at + lane < p.sel_k ? p.sel_logical[i] : -1;
-        ids = pages >= 0 ? p.sel_phys[i] : -1;
+        const bool there = at + lane < p.sel_k;
+        pages = there ? p.sel_logical[i] : -1;
+        ids = there ? p.sel_phys[i] : -1;
         if (pages >= (rq.held + TT - 1) / TT) {        // no token of the request
           report(a.err, QUEST_DEVERR_EMPTY_PAGE);
           pages = -1;

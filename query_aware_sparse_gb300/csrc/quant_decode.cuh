@@ -150,4 +150,210 @@ template <int D, int S> struct WarpE4M3 : WarpMma<D> {
   }
 };
 
+// ---------------------------------------------------------------------------
+// Few tiles: a cluster of up to eight CTAs of four warps takes one unit, its
+// parts meet in distributed shared memory, and one launch is all there is.
+// ---------------------------------------------------------------------------
+constexpr int kUnitWarps = 4, kUnitCtasPerSm = 3;
+
+template <int D, int S> struct UnitShape {
+  static constexpr uint32_t STAGE = RecordShape<D, S>::STAGE;
+  static constexpr int STAGES = 66560 / kUnitWarps / STAGE;
+  static constexpr uint32_t RING = STAGES * STAGE, SMEM = kUnitWarps * RING;
+  static_assert(STAGES <= 32 && kUnitCtasPerSm * (SMEM + 3072) <= 227 * 1024, "three CTAs per SM");
+  // a part (o and m, l of up to eight heads) behind a part, in a ring that is through
+  static constexpr uint32_t PART = 8 * D * 4 + 8 * 8;
+  static_assert(2 * PART <= RING && PART % 16 == 0, "parts use the rings");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t at, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+
+// Joins N parts' four dims: m, l and o of part i from ml(i) and o(i).
+template <int N, typename M, typename O>
+__device__ __forceinline__ void join_four(int n, M ml, O o, float& m, float& l, float4& sum) {
+  float2 x[N];
+  float4 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = make_float2(-INFINITY, 0.f);
+    v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n) { x[i] = ml(i); v[i] = o(i); }
+  }
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmaxf(m, x[i].x);
+  l = 0.f;
+  sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m == -INFINITY) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float f = ex2(x[i].x - m);
+    l = fmaf(f, x[i].y, l);
+    sum.x = fmaf(f, v[i].x, sum.x);
+    sum.y = fmaf(f, v[i].y, sum.y);
+    sum.z = fmaf(f, v[i].z, sum.z);
+    sum.w = fmaf(f, v[i].w, sum.w);
+  }
+}
+
+// LIST as above. Grid: a cluster (of gridDim-independent size) per unit.
+template <int D, int S, bool LIST>
+__global__ void __launch_bounds__(kUnitWarps * 32, kUnitCtasPerSm)
+quant_unit_kernel(const PageRecords source, const DecodeArgs p) {
+  using W = WarpE4M3<D, S>;
+  using Sh = UnitShape<D, S>;
+  constexpr int NST = Sh::STAGES;
+  extern __shared__ __align__(128) uint8_t unit_smem[];
+  __shared__ __align__(8) uint64_t s_bar[kUnitWarps][NST];
+  __shared__ int s_tok[kUnitWarps][NST];
+  const DenseArgs& a = p.a;
+  const int G = a.group, warp = __shfl_sync(FULL, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  int ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
+  const int unit = blockIdx.x / ctas, r = unit / a.h_kv, g = unit % a.h_kv;
+  const uint32_t smem = smem_u32(unit_smem), ring = smem + warp * Sh::RING;
+  if (lane < NST) mbar_init(&s_bar[warp][lane], 1);
+  fence_mbar_init();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // The warp's tiles: every (4 ctas)-th of the unit's, 32 of them looked up at
+  // a time, one per lane; those without a page or a token are left out there.
+  const int step = kUnitWarps * ctas, own = rank * kUnitWarps + warp;
+  int at = own, pages = -1, ids = -1;
+  const size_t list = (size_t)unit * p.sel_k;
+  if (LIST && at + lane * step < p.sel_k) {            // on the way beside the length
+    pages = p.sel_logical[list + at + lane * step];
+    ids = p.sel_phys[list + at + lane * step];
+  }
+  W w;
+  w.begin(a, r, g, lane, nullptr);
+  unsigned* err = own == 0 && g == 0 ? a.err : nullptr;
+  const Request rq = LIST ? listed_request(p, r) : request_of<S>(a, r, err);
+  unsigned left = 0;
+  auto look_up = [&](bool first) {
+    const int i = at + lane * step;
+    at += 32 * step;
+    if constexpr (LIST) {
+      if (!first) {
+        pages = i < rq.tiles ? p.sel_logical[list + i] : -1;
+        ids = i < rq.tiles ? p.sel_phys[list + i] : -1;
+      }
+      if (pages >= (rq.held + S - 1) / S) {            // no token of the request
+        report(a.err, QUEST_DEVERR_EMPTY_PAGE);
+        pages = -1;
+      }
+    } else {
+      pages = i < rq.tiles ? rq.tile0 + i : -1;
+      ids = i < rq.tiles ? a.page_indices[rq.e0 + rq.tile0 + i] : -1;
+    }
+    if (pages >= 0 && (ids < 0 || ids >= a.n_phys)) {
+      report(a.err, QUEST_DEVERR_PAGE_RANGE);
+      pages = -1;
+    }
+    left = __ballot_sync(FULL, pages >= 0);
+  };
+  look_up(true);
+
+  const uint64_t pol = evict_first_policy();
+  const bool fault = a.test_fault == 2 && blockIdx.x == 0 && warp == 0;
+  int issued = 0;
+  auto issue = [&] {                                   // the next tile into the ring
+    while (!left && at < rq.tiles) look_up(false);
+    if (!left) return;
+    const int src = __ffs(left) - 1, st = issued % NST;
+    left &= left - 1;
+    const int id = __shfl_sync(FULL, ids, src), lp = __shfl_sync(FULL, pages, src);
+    if (lane == 0) {
+      s_tok[warp][st] = lp * S;
+      mbar_expect_tx(&s_bar[warp][st], Sh::STAGE + (fault && issued == 0 ? 16 : 0));
+      W::copy(source, a, id, g, 0, ring + st * Sh::STAGE, &s_bar[warp][st], pol);
+    }
+    ++issued;
+  };
+  for (int k = 0; k < NST; ++k) issue();
+  const float scale2 = a.scale * LOG2E;
+  int done = 0, st = 0;
+  uint32_t phase = 0;
+  for (; done < issued; ++done) {
+    __syncwarp();
+    if (!warp_wait_bounded(&s_bar[warp][st], phase >> st & 1, p.wait_limit)) break;
+    phase ^= 1u << st;
+    w.tile(a, rq, s_tok[warp][st], ring + st * Sh::STAGE, nullptr, scale2, lane);
+    __syncwarp();
+    issue();
+    if (++st == NST) st = 0;
+  }
+  if (done < issued) {                                 // report, and wait for the copies in flight
+    if (lane == 0) report(a.err, QUEST_DEVERR_WAIT_TIMEOUT);
+    for (int k = done; k < issued; ++k, st = st + 1 == NST ? 0 : st + 1)
+      warp_wait_bounded(&s_bar[warp][st], phase >> st & 1, p.wait_limit);
+  }
+
+  // the warp's part into its ring, the CTA's behind the first warp's
+  auto o_at = [&](uint32_t part, int h) { return part + h * D * 4; };
+  auto ml_at = [&](uint32_t part, int h) { return part + G * D * 4 + h * 8; };
+  w.finish(a, false, lane, [&](int h, float m, float l, bool mine) {
+    float* o = reinterpret_cast<float*>(unit_smem + warp * Sh::RING);
+    if (mine) *reinterpret_cast<float2*>(o + G * D + 2 * h) = make_float2(m, l);
+    return o + h * D;
+  });
+  __syncthreads();
+  const size_t row = (size_t)unit * G;
+  auto put = [&](int h, int d4, float m, float l, float4 o) {
+    const float f = l > 0.f ? 1.f / l : 0.f;
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (row + h) * D + d4 * 4) =
+        make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    if (d4 == 0 && a.lse) a.lse[row + h] = l > 0.f ? (m - 6.f + lg2(l)) * LN2 : -INFINITY;
+  };
+  const int items = G * (D / 4);
+  const uint32_t cta_part = smem + Sh::PART;
+  for (int i = threadIdx.x; i < items; i += kUnitWarps * 32) {
+    const int h = i / (D / 4), d4 = i % (D / 4);
+    float m, l;
+    float4 o;
+    join_four<kUnitWarps>(kUnitWarps, [&](int k) { return ld_cluster2(in_cta(ml_at(smem + k * Sh::RING, h), rank)); },
+                          [&](int k) { return ld_cluster4(in_cta(o_at(smem + k * Sh::RING, h) + d4 * 16, rank)); }, m, l, o);
+    if (ctas == 1) {
+      put(h, d4, m, l, o);
+    } else {
+      float* to = reinterpret_cast<float*>(unit_smem + Sh::PART);
+      *reinterpret_cast<float4*>(to + h * D + d4 * 4) = o;
+      if (d4 == 0) *reinterpret_cast<float2*>(to + G * D + 2 * h) = make_float2(m, l);
+    }
+  }
+  if (ctas == 1) return;
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int i = rank * kUnitWarps * 32 + threadIdx.x; i < items; i += ctas * kUnitWarps * 32) {
+    const int h = i / (D / 4), d4 = i % (D / 4);
+    float m, l;
+    float4 o;
+    join_four<8>(ctas, [&](int k) { return ld_cluster2(in_cta(ml_at(cta_part, h), k)); },
+                 [&](int k) { return ld_cluster4(in_cta(o_at(cta_part, h) + d4 * 16, k)); }, m, l, o);
+    put(h, d4, m, l, o);
+  }
+  // a CTA's part stays until every other has read it
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 }  // namespace quest

@@ -56,22 +56,33 @@ inline int sm_count() {
 }
 
 // A launch that may begin before the kernel in front of it on the stream has
-// ended (it waits with pdl_wait).
+// ended (it waits with pdl_wait), in clusters of `ctas` CTAs where that is not 0.
 template <typename K, typename... A>
-inline cudaError_t launch_pdl(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
-                              A... args) {
+inline cudaError_t launch_pdl_clusters(K kernel, unsigned grid, unsigned ctas, unsigned threads, size_t smem,
+                                       cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
+  cudaLaunchAttribute attr[2];
   static const bool off = getenv("QUEST_NO_PDL") != nullptr;
-  cfg.numAttrs = off ? 0 : 1;
+  if (!off) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (ctas) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = ctas;
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  cfg.attrs = attr;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename K, typename... A>
+inline cudaError_t launch_pdl(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  return launch_pdl_clusters(kernel, grid, 0, threads, smem, s, args...);
 }
 
 }  // namespace quest
