@@ -595,32 +595,51 @@ class QKNorm:
 
     def __init__(self, q_weight, k_weight, eps: float = 1e-6):
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+        self.sides = []                 # (name, heads or 0 for all, dims, device) of each weight
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                if w.dim() not in (1, 2):
+                    raise ValueError(f"{name} must be [d] or [heads, d], not {tuple(w.shape)}")
+                _expect(name, w, torch.float32, tuple(w.shape), w.get_device())
+                self.sides.append((name, w.shape[0] if w.dim() == 2 else 0, w.shape[-1], w.get_device()))
         per_head = [int(w is not None and w.dim() == 2) for w in (q_weight, k_weight)]
         self.c = QuestQKNorm(_ptr(q_weight), _ptr(k_weight), *per_head, self.eps)
 
     def check(self, h_q, h_kv, d, device):
-        for name, w, heads in (("q_weight", self.q_weight, h_q), ("k_weight", self.k_weight, h_kv)):
-            if w is not None:
-                _expect(name, w, torch.float32, (heads, d) if w.dim() == 2 else (d,), device)
+        for name, heads, dims, dev in self.sides:
+            if dims != d or dev != device or heads and heads != (h_q if name == "q_weight" else h_kv):
+                raise ValueError(f"{name} must have {d} dims for {h_q} query and {h_kv} KV heads on CUDA device "
+                                 f"{device}, not {dims} for {heads or 'all'} heads on {dev}")
 
 
 def _append_args(cache, table, q, k_new, v_new, append_indptr, seq_lens_before, inv_freq, group,
                  q_out, positions, interleaved, stream, dev):
     """Checks what the normed and the E4M3 append share: (QuestRope or None,
-    q_out, the arguments of the C calls from q on)."""
-    dt, n = cache.dtype, k_new.shape[0]
-    h, d = cache.h_kv, cache.head_dim
-    kv = (n, h, d)
-    k_stride = _expect_rows("k_new", k_new, dt, kv, dev)
-    v_stride = _expect_rows("v_new", v_new, dt, kv, dev)
-    _expect("append_indptr", append_indptr, torch.int32, (table.batch + 1,), dev)
-    _expect("seq_lens_before", seq_lens_before, torch.int32, (table.batch,), dev)
+    q_out, the arguments of the C calls from q on). In a decode loop the calls
+    are bound by these checks on the host, so what is as usual is looked at in
+    one place, and the helpers only where something is not."""
+    dt, h, d, i32 = cache.dtype, cache.h_kv, cache.head_dim, torch.int32
+    kv = k_new.shape
+    n = kv[0]
+    (ks, k1, k2), (vs, v1, v2) = k_new.stride(), v_new.stride()
+    if not (n > 1 and kv == (n, h, d) and v_new.shape == kv and k_new.dtype is dt and v_new.dtype is dt and
+            k_new.get_device() == dev and v_new.get_device() == dev and
+            k2 == v2 == 1 and k1 == v1 == d and ks >= h * d and vs >= h * d):
+        ks = _expect_rows("k_new", k_new, dt, (n, h, d), dev)
+        vs = _expect_rows("v_new", v_new, dt, (n, h, d), dev)
+    B = table.batch
+    if not (append_indptr.dtype is i32 and append_indptr.shape == (B + 1,) and append_indptr.get_device() == dev and
+            append_indptr.is_contiguous() and seq_lens_before.dtype is i32 and seq_lens_before.shape == (B,) and
+            seq_lens_before.get_device() == dev and seq_lens_before.is_contiguous()):
+        _expect("append_indptr", append_indptr, i32, (B + 1,), dev)
+        _expect("seq_lens_before", seq_lens_before, i32, (B,), dev)
     rope = None
     if inv_freq is not None:
-        _expect("inv_freq", inv_freq, torch.float64, (inv_freq.numel(),), dev)
+        half = inv_freq.numel()
+        _expect("inv_freq", inv_freq, torch.float64, (half,), dev)
         if positions is not None:
-            _expect("positions", positions, torch.int32, (n,), dev)
-        rope = QuestRope(_ptr(inv_freq), _ptr(positions), 2 * inv_freq.numel(), int(bool(interleaved)))
+            _expect("positions", positions, i32, (n,), dev)
+        rope = QuestRope(inv_freq.data_ptr(), _ptr(positions), 2 * half, 1 if interleaved else 0)
     elif positions is not None:
         raise ValueError("positions need inv_freq")
     q_stride = 0
@@ -632,8 +651,8 @@ def _append_args(cache, table, q, k_new, v_new, append_indptr, seq_lens_before, 
         _expect("q_out", q_out, dt, rows, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    return rope, q_out, (_ptr(q), _ptr(k_new), _ptr(v_new), q_stride, k_stride, v_stride, n, int(group),
-                         _ptr(append_indptr), _ptr(seq_lens_before), _ptr(q_out), _raw_stream(stream, dev))
+    return rope, q_out, (_ptr(q), k_new.data_ptr(), v_new.data_ptr(), q_stride, ks, vs, n, group,
+                         append_indptr.data_ptr(), seq_lens_before.data_ptr(), _ptr(q_out), _raw_stream(stream, dev))
 
 
 def norm_rope_append_kv(cache: PagedCache, table: PageTable, q, k_new, v_new, append_indptr,
@@ -697,14 +716,20 @@ def quant_decode_workspace_size(batch, h_kv, group, head_dim, page_size) -> int:
 
 
 def _quant_decode_args(cache, table, q, group, out, lse, workspace, stream, dev):
+    """(out, lse, workspace) of a decode call, checked (as in _append_args)."""
+    f32 = torch.float32
     B, h_q, d = table.batch, cache.h_kv * group, cache.head_dim
-    _expect("q", q, torch.float16, (B, h_q, d), dev)
+    rows, heads = (B, h_q, d), (B, h_q)
     if out is None:
-        out = _result((B, h_q, d), torch.float32, dev, stream)
+        out = _result(rows, f32, dev, stream)
     if lse is None:
-        lse = _result((B, h_q), torch.float32, dev, stream)
-    _expect("out", out, torch.float32, (B, h_q, d), dev)
-    _expect("lse", lse, torch.float32, (B, h_q), dev)
+        lse = _result(heads, f32, dev, stream)
+    if not (q.dtype is torch.float16 and out.dtype is f32 and lse.dtype is f32 and q.shape == rows and
+            out.shape == rows and lse.shape == heads and q.is_contiguous() and out.is_contiguous() and
+            lse.is_contiguous() and q.get_device() == dev and out.get_device() == dev and lse.get_device() == dev):
+        _expect("q", q, torch.float16, rows, dev)
+        _expect("out", out, f32, rows, dev)
+        _expect("lse", lse, f32, heads, dev)
     if workspace is None:
         workspace = _scratch(quant_decode_workspace_size(B, cache.h_kv, group, d, cache.page_size), dev, stream)
     _expect_workspace(workspace, dev)
@@ -718,13 +743,17 @@ def quant_sparse_decode_attn(cache: QuantCache, table: PageTable, q, group: int,
     over the pages that select_topk chose (int32 [B, h_kv, k]). ``workspace``:
     uint8, quant_decode_workspace_size bytes."""
     dev = _current(cache, table)
-    for name, sel in (("sel_logical", sel_logical), ("sel_phys", sel_phys)):
-        _expect(name, sel, torch.int32, (table.batch, cache.h_kv, k), dev)
+    lists, i32 = (table.batch, cache.h_kv, k), torch.int32
+    if not (sel_logical.dtype is i32 and sel_phys.dtype is i32 and sel_logical.shape == lists and
+            sel_phys.shape == lists and sel_logical.is_contiguous() and sel_phys.is_contiguous() and
+            sel_logical.get_device() == dev and sel_phys.get_device() == dev):
+        _expect("sel_logical", sel_logical, i32, lists, dev)
+        _expect("sel_phys", sel_phys, i32, lists, dev)
     out, lse, workspace = _quant_decode_args(cache, table, q, group, out, lse, workspace, stream, dev)
     _check(lib().quest_quant_sparse_decode_attn(
-        ctypes.byref(cache.quant), ctypes.byref(table.c), _ptr(q), int(group), _ptr(sel_logical),
-        _ptr(sel_phys), int(k), _ptr(out), _ptr(lse), float(sm_scale), _ptr(workspace),
-        int(workspace.numel() * workspace.element_size()), _raw_stream(stream, dev)))
+        ctypes.byref(cache.quant), ctypes.byref(table.c), q.data_ptr(), group, sel_logical.data_ptr(),
+        sel_phys.data_ptr(), k, out.data_ptr(), lse.data_ptr(), sm_scale, workspace.data_ptr(), workspace.nbytes,
+        _raw_stream(stream, dev)))
     return out, lse
 
 
@@ -739,9 +768,9 @@ def quant_dense_decode_attn(cache: QuantCache, table: PageTable, q, group: int, 
         mods.check(cache.h_kv * group, table.batch, table.batch, dev)
     out, lse, workspace = _quant_decode_args(cache, table, q, group, out, lse, workspace, stream, dev)
     _check(lib().quest_quant_dense_decode_attn(
-        ctypes.byref(cache.quant), ctypes.byref(table.c), _ptr(q), int(group),
-        None if mods is None else ctypes.byref(mods.c), _ptr(out), _ptr(lse), float(sm_scale),
-        _ptr(workspace), int(workspace.numel() * workspace.element_size()), _raw_stream(stream, dev)))
+        ctypes.byref(cache.quant), ctypes.byref(table.c), q.data_ptr(), group,
+        None if mods is None else ctypes.byref(mods.c), out.data_ptr(), lse.data_ptr(), sm_scale,
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)))
     return out, lse
 
 

@@ -156,6 +156,26 @@ template <int D> struct WarpMma {
     since = 0;
   }
 
+  // The weights of a group whose products are still to come, after another
+  // group's maximum has taken the place of m0, m1.
+  __device__ __forceinline__ void reweigh(float m0, float m1, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
+    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m[0]), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m[1]);
+    // of column lane / 4: kept by lane t = column / 2
+    const float a = __shfl_sync(FULL, f0, lane >> 3), b = __shfl_sync(FULL, f1, lane >> 3);
+    const float f = lane & 4 ? b : a;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&lo[i]));
+      const float2 v = make_float2((x.x + y.x) * f, (x.y + y.y) * f);
+      const __half2 h = __floats2half2_rn(v.x, v.y);
+      const float2 back = __half22float2(h);
+      const __half2 rest = __floats2half2_rn(v.x - back.x, v.y - back.y);
+      hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+      lo[i] = *reinterpret_cast<const uint32_t*>(&rest);
+    }
+  }
+
   // Products s of tokens tok0 .. tok0 + 15 -> their weights, as the two halves
   // of P^T (k index of a half: 2 t, 2 t + 1 (+ 8)).
   __device__ __forceinline__ void weigh(const DenseArgs& a, const Request& rq, int tok0, const float (&s)[4],
@@ -175,7 +195,7 @@ template <int D> struct WarpMma {
       for (int c = 0; c < 4; ++c) x[c] = s[c] * scale2;
     }
     const bool edge = tok0 < rq.lo || tok0 + 16 > rq.hi;
-    if (edge) {
+    if (edge) {                                        // (tok0 may be a lane's own)
       if (ta < rq.lo || ta >= rq.hi) x[0] = x[1] = -INFINITY;
       if (tb < rq.lo || tb >= rq.hi) x[2] = x[3] = -INFINITY;
     }

@@ -20,9 +20,9 @@ Plan plan_quant(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim) {
   return p;
 }
 
-template <int D, int S, bool LIST>
+template <int D, int S, bool LIST, bool PACK>
 cudaError_t launch(const DecodeArgs& p, cudaStream_t s) {
-  using W = WarpE4M3<D, S>;
+  using W = WarpE4M3<D, S, PACK>;
   using Sh = typename W::Shape;
   static_assert(Sh::WARPS == RecordShape<D, 16>::WARPS, "one plan for both page sizes");
   cudaError_t e = cudaFuncSetAttribute(dense_decode_kernel<W, D, LIST>,
@@ -60,19 +60,21 @@ template <bool LIST> int unit_ctas(const DecodeArgs& p) {
   return waves * tiles <= (units * c >= sms ? 20 : 12) ? c : 0;
 }
 
-template <int D, int S, bool LIST>
+template <int D, int S, bool LIST, bool PACK>
 cudaError_t launch_units(const DecodeArgs& p, int ctas, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(quant_unit_kernel<D, S, LIST>,
+  const cudaError_t e = cudaFuncSetAttribute(quant_unit_kernel<D, S, LIST, PACK>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, UnitShape<D, S>::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl_clusters(quant_unit_kernel<D, S, LIST>, (unsigned)p.a.batch * p.a.h_kv * ctas, ctas,
+  return launch_pdl_clusters(quant_unit_kernel<D, S, LIST, PACK>, (unsigned)p.a.batch * p.a.h_kv * ctas, ctas,
                              kUnitWarps * 32, UnitShape<D, S>::SMEM, s,
                              PageRecords{static_cast<const uint8_t*>(p.a.k_pool)}, p);
 }
 
 template <int D, int S, bool LIST> cudaError_t launch_either(const DecodeArgs& p, cudaStream_t s) {
   const int ctas = unit_ctas<LIST>(p);
-  return ctas ? launch_units<D, S, LIST>(p, ctas, s) : launch<D, S, LIST>(p, s);
+  if constexpr (S == 32)
+    if (p.a.group <= 4) return ctas ? launch_units<D, S, LIST, true>(p, ctas, s) : launch<D, S, LIST, true>(p, s);
+  return ctas ? launch_units<D, S, LIST, false>(p, ctas, s) : launch<D, S, LIST, false>(p, s);
 }
 
 template <bool LIST> cudaError_t launch_shape(const DecodeArgs& p, cudaStream_t s) {
