@@ -1,5 +1,6 @@
 // Decode attention over the E4M3 cache: plan and launch (quant_decode.cuh).
 #include <algorithm>
+#include <atomic>
 
 #include "quant_decode.cuh"
 #include "internal.h"
@@ -38,26 +39,57 @@ cudaError_t launch(const DecodeArgs& p, cudaStream_t s) {
   return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, kJoinThreads, 0, s, p);
 }
 
+// Clusters of 1 to 8 CTAs of a kernel that the current device keeps at once
+// (asked for once per device; the driver packs them into its GPCs).
+template <typename K> int resident_clusters(K kernel, int ctas, size_t smem, std::atomic<int> (&known)[64][9]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+  int n = known[dev][ctas].load();
+  if (n) return n;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kUnitWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  known[dev][ctas].store(n > 0 ? n : -1);
+  return n;
+}
+
 // CTAs of a unit's cluster: as many as the device holds at once for all units,
 // with a tile for each warp. 0: the equal runs serve the call better, which cost
 // 5 us more to start and join, but leave no warp with more tiles than another.
-// A warp's tiles one after the other take 0.6 us each (latency) or, from a CTA
-// per SM on, what HBM gives them. us, clusters and runs (128 dims, pages of 16):
-//   1 head, 31 / 250 / 500 / 1000 pages   3.8 / 7.9 / 12.8 / 22   9.0 / 10.7 / 11.5 / 12.6
-//   32 heads, 125 / 250 / 500 / 1000      7.6 / 11.6 / 18.6 / 33  11.9 / 16.9 / 21.9 / 31.7
-//   16 requests of 8 heads, 32 / 128 / 256 / 512 listed   7.8 / 18.5 / 32 / 61   11.8 / 21.3 / 30 / 50
-//   64 of 8, 8 / 32 / 128 (two waves)     8.0 / 19.6 / 63         12.2 / 21.1 / 50
+// A warp's tiles one after the other take 0.6 us each (latency) or, where the
+// SMs are full, what HBM gives them. us, clusters and runs (128 dims, pages of 16):
+//   1 head, 31 / 250 / 500 / 1000 pages          3.6 / 7.5 / 12.8 / 22     9.0 / 10.5 / 11.4 / 12.4
+//   32 heads, 125 / 250 / 500 / 1000             7.4 / 11.3 / 18 / 33      11.9 / 16.9 / 21.8 / 31.5
+//   16 requests of 8 heads, 64 / 256 / 512       10.2 / 25.2 / 45.4        16.0 / 30.5 / 50.4
+//   60 requests of 8 heads (two waves), 32 / 64 / 128   18.3 / 31.5 / 58   20.6 / 29.2 / 47.6
 // Tables: the host knows no lengths, so all pages may be one request's, unless a
 // window bounds what is read.
-template <bool LIST> int unit_ctas(const DecodeArgs& p) {
+template <int D, int S, bool LIST, bool PACK> int unit_ctas(const DecodeArgs& p) {
   const long long units = (long long)p.a.batch * p.a.h_kv;
   long long most = LIST ? p.sel_k : p.a.nnz;
   if (!LIST && p.a.window > 0) most = std::min<long long>(most, (p.a.window - 1) / p.a.page_size + 2);
-  const int sms = sm_count(), slots = kUnitCtasPerSm * sms;
+  static std::atomic<int> known[64][9];
+  auto resident = [&](int c) {
+    return resident_clusters(quant_unit_kernel<D, S, LIST, PACK>, c, UnitShape<D, S>::SMEM, known);
+  };
   int c = 8;
-  while (c > 1 && (units * c > slots || most < kUnitWarps * c)) c /= 2;
-  const long long waves = (units * c + slots - 1) / slots, tiles = (most + kUnitWarps * c - 1) / (kUnitWarps * c);
-  return waves * tiles <= (units * c >= sms ? 20 : 12) ? c : 0;
+  while (c > 1 && (most < kUnitWarps * c || units > resident(c))) --c;
+  const int n = resident(c), sms = sm_count();
+  if (n <= 0) return 0;
+  const long long waves = (units + n - 1) / n, tiles = (most + kUnitWarps * c - 1) / (kUnitWarps * c);
+  return waves * tiles <= (waves > 1 ? 16 : units * c >= 2 * sms ? 64 : units * c >= sms ? 20 : 12) ? c : 0;
 }
 
 template <int D, int S, bool LIST, bool PACK>
@@ -70,17 +102,16 @@ cudaError_t launch_units(const DecodeArgs& p, int ctas, cudaStream_t s) {
                              PageRecords{static_cast<const uint8_t*>(p.a.k_pool)}, p);
 }
 
-template <int D, int S, bool LIST> cudaError_t launch_either(const DecodeArgs& p, cudaStream_t s) {
-  const int ctas = unit_ctas<LIST>(p);
-  if constexpr (S == 32)
-    if (p.a.group <= 4) return ctas ? launch_units<D, S, LIST, true>(p, ctas, s) : launch<D, S, LIST, true>(p, s);
-  return ctas ? launch_units<D, S, LIST, false>(p, ctas, s) : launch<D, S, LIST, false>(p, s);
+template <int D, int S, bool LIST, bool PACK> cudaError_t launch_either(const DecodeArgs& p, cudaStream_t s) {
+  const int ctas = unit_ctas<D, S, LIST, PACK>(p);
+  return ctas ? launch_units<D, S, LIST, PACK>(p, ctas, s) : launch<D, S, LIST, PACK>(p, s);
 }
 
 template <bool LIST> cudaError_t launch_shape(const DecodeArgs& p, cudaStream_t s) {
-  if (p.a.head_dim == 128)
-    return p.a.page_size == 16 ? launch_either<128, 16, LIST>(p, s) : launch_either<128, 32, LIST>(p, s);
-  return p.a.page_size == 16 ? launch_either<64, 16, LIST>(p, s) : launch_either<64, 32, LIST>(p, s);
+  const bool d128 = p.a.head_dim == 128;
+  if (p.a.page_size == 16) return d128 ? launch_either<128, 16, LIST, false>(p, s) : launch_either<64, 16, LIST, false>(p, s);
+  if (p.a.group <= 4) return d128 ? launch_either<128, 32, LIST, true>(p, s) : launch_either<64, 32, LIST, true>(p, s);
+  return d128 ? launch_either<128, 32, LIST, false>(p, s) : launch_either<64, 32, LIST, false>(p, s);
 }
 
 }  // namespace
