@@ -673,12 +673,12 @@ dense_decode_kernel(const __grid_constant__ typename W::Source source, const Dec
 
 // Joins the parts of one (request, query head): the threads take the parts'
 // maxima and sums and leave each part's weight in shared memory, then the warps
-// every eighth part's o (loads without anything to wait for), whose sums meet
+// their share of the parts' o (loads without anything to wait for), whose sums meet
 // in shared memory, in a fixed order.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) dense_decode_join_kernel(const DecodeArgs p) {
-  constexpr int E = D / 32, CHUNK = 1024;
+constexpr int kJoinThreads = 256;
+template <int D, int NT = kJoinThreads>
+__global__ void __launch_bounds__(NT) dense_decode_join_kernel(const DecodeArgs p) {
+  constexpr int E = D / 32, CHUNK = 1024, kJoinWarps = NT / 32;
   __shared__ float s_o[kJoinWarps][D], s_w[CHUNK], s_red[2][kJoinWarps];
   const DenseArgs& a = p.a;
   pdl_wait();
@@ -700,11 +700,11 @@ __global__ void __launch_bounds__(kJoinThreads) dense_decode_join_kernel(const D
   float m = -INFINITY, l = 0.f, o[E] = {};
   for (int c0 = 0; c0 < parts; c0 += CHUNK) {
     const int cnt = min(CHUNK, parts - c0);
-    float2 ml[CHUNK / kJoinThreads];
+    float2 ml[CHUNK / NT];
     float mx = m;
 #pragma unroll
-    for (int k = 0; k < CHUNK / kJoinThreads; ++k) {
-      const int i = k * kJoinThreads + threadIdx.x;
+    for (int k = 0; k < CHUNK / NT; ++k) {
+      const int i = k * NT + threadIdx.x;
       ml[k] = i < cnt ? p.part_ml[slot0 + (size_t)(c0 + i) * a.group] : make_float2(-INFINITY, 0.f);
       mx = fmaxf(mx, ml[k].x);
     }
@@ -717,8 +717,8 @@ __global__ void __launch_bounds__(kJoinThreads) dense_decode_join_kernel(const D
     if (mx == -INFINITY) continue;                     // parts without a key (whole CTA)
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < CHUNK / kJoinThreads; ++k) {
-      const int i = k * kJoinThreads + threadIdx.x;
+    for (int k = 0; k < CHUNK / NT; ++k) {
+      const int i = k * NT + threadIdx.x;
       const float f = ex2(ml[k].x - mx);
       if (i < cnt) s_w[i] = f;
       sum = fmaf(f, ml[k].y, sum);

@@ -21,6 +21,13 @@ Plan plan_quant(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim) {
   return p;
 }
 
+template <int D, int NT> cudaError_t launch_join(const DecodeArgs& p, unsigned rows, cudaStream_t s) {
+  // the same shared memory split as the kernel before it
+  const cudaError_t e = cudaFuncSetAttribute(dense_decode_join_kernel<D, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+  return e == cudaSuccess ? launch_pdl(dense_decode_join_kernel<D, NT>, rows, NT, 0, s, p) : e;
+}
+
 template <int D, int S, bool LIST, bool PACK>
 cudaError_t launch(const DecodeArgs& p, cudaStream_t s) {
   using W = WarpE4M3<D, S, PACK>;
@@ -32,11 +39,9 @@ cudaError_t launch(const DecodeArgs& p, cudaStream_t s) {
   const PageRecords src{static_cast<const uint8_t*>(p.a.k_pool)};
   e = launch_pdl(dense_decode_kernel<W, D, LIST>, p.n_warps / Sh::WARPS, Sh::WARPS * 32, Sh::SMEM, s, src, p);
   if (e != cudaSuccess) return e;
-  // the same shared memory split as the kernel before it
-  e = cudaFuncSetAttribute(dense_decode_join_kernel<D>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(dense_decode_join_kernel<D>, (unsigned)p.a.batch * p.a.h_kv * p.a.group, kJoinThreads, 0, s, p);
+  // few units have many parts: more warps take them
+  const unsigned rows = (unsigned)p.a.batch * p.a.h_kv * p.a.group;
+  return p.n_warps > 64 * p.a.batch * (long long)p.a.h_kv ? launch_join<D, 1024>(p, rows, s) : launch_join<D, kJoinThreads>(p, rows, s);
 }
 
 // Clusters of 1 to 8 CTAs of a kernel that the current device keeps at once
