@@ -177,7 +177,9 @@ template <int D> struct WarpMma {
   }
 
   // Products s of tokens tok0 .. tok0 + 15 -> their weights, as the two halves
-  // of P^T (k index of a half: 2 t, 2 t + 1 (+ 8)).
+  // of P^T (k index of a half: 2 t, 2 t + 1 (+ 8)). JOINT: columns c and c + 4
+  // are of the same head and keep the same maximum.
+  template <bool JOINT = false>
   __device__ __forceinline__ void weigh(const DenseArgs& a, const Request& rq, int tok0, const float (&s)[4],
                                         float scale2, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
     const int ta = tok0 + (lane >> 2), tb = ta + 8;
@@ -205,7 +207,7 @@ template <int D> struct WarpMma {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int o = 4; o <= 16; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(FULL, mx[i], o));
+        for (int o = JOINT ? 2 : 4; o <= 16; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(FULL, mx[i], o));
         if (mx[i] > m[i]) {
           const float f = ex2(m[i] - mx[i]);           // first maximum: 0, and o and l are 0
           m[i] = mx[i];

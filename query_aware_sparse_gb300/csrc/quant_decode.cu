@@ -112,11 +112,13 @@ template <int D, int S, bool LIST, bool PACK> cudaError_t launch_either(const De
   return ctas ? launch_units<D, S, LIST, PACK>(p, ctas, s) : launch<D, S, LIST, PACK>(p, s);
 }
 
-template <bool LIST> cudaError_t launch_shape(const DecodeArgs& p, cudaStream_t s) {
-  const bool d128 = p.a.head_dim == 128;
-  if (p.a.page_size == 16) return d128 ? launch_either<128, 16, LIST, false>(p, s) : launch_either<64, 16, LIST, false>(p, s);
-  if (p.a.group <= 4) return d128 ? launch_either<128, 32, LIST, true>(p, s) : launch_either<64, 32, LIST, true>(p, s);
-  return d128 ? launch_either<128, 32, LIST, false>(p, s) : launch_either<64, 32, LIST, false>(p, s);
+template <bool LIST, bool PACK> cudaError_t launch_shape(const DecodeArgs& p, cudaStream_t s) {
+  if (p.a.head_dim == 128)
+    return p.a.page_size == 16 ? launch_either<128, 16, LIST, PACK>(p, s) : launch_either<128, 32, LIST, PACK>(p, s);
+  return p.a.page_size == 16 ? launch_either<64, 16, LIST, PACK>(p, s) : launch_either<64, 32, LIST, PACK>(p, s);
+}
+template <bool LIST> cudaError_t launch_group(const DecodeArgs& p, cudaStream_t s) {
+  return p.a.group <= 4 ? launch_shape<LIST, true>(p, s) : launch_shape<LIST, false>(p, s);
 }
 
 }  // namespace
@@ -140,7 +142,7 @@ cudaError_t launch_quant_decode(const DenseArgs& a, const int32_t* sel_logical, 
   p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
   p.n_warps = plan.warps;
   p.wait_limit = wait_limit();
-  return sel_logical ? launch_shape<true>(p, s) : launch_shape<false>(p, s);
+  return sel_logical ? launch_group<true>(p, s) : launch_group<false>(p, s);
 }
 
 }  // namespace quest

@@ -34,12 +34,12 @@ template <int D, int S> struct RecordShape {
 //
 // The two groups of 16 tokens of a 32-token page go through together, so that
 // one's chain of loads, products and shuffles hides the other's. PACK (up to
-// four heads, such pages): the heads stand in the MMA's columns twice, the first
-// group's logits are taken from columns 0..3 and the second's from 4..7, and one
-// softmax step serves both; a head's two columns keep a maximum and a sum each
-// and are joined at the end. (64 dims, 63 requests of up to 8192 tokens, capped:
-// 24.2 -> 22.7 us; 16000 tokens of one head 15.4 -> 11.7. Two pages of 16 tokens
-// together gained nothing: their copies are waited for, not their arithmetic.)
+// four heads): the heads stand in the MMA's columns twice. The first group's
+// logits are taken from columns 0..3 and the second's from 4..7, one softmax
+// step serves both, and the two halves of a weight meet a group's values in one
+// product, in a column each. What a head's two columns hold adds up at the end.
+// (64 dims, 63 requests of up to 8192 tokens, capped: 24.2 us without; 16000
+// tokens of one head 15.4 -> 11.7. Two pages of 16 tokens together gained nothing.)
 template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
   using Base = WarpMma<D>;
   using Shape = RecordShape<D, S>;
@@ -127,17 +127,17 @@ template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
     }
     return v;
   }
-  // acc += V^T P^T of 16 tokens and 32 dims.
-  __device__ __forceinline__ void add(uint32_t rec, int sub, int i, int lane, const Values& v, const uint32_t (&hi)[2],
-                                      const uint32_t (&lo)[2]) {
+  // acc += V^T P^T of 16 tokens and 32 dims, for N columns' halves of weights.
+  template <int N>
+  __device__ __forceinline__ void add(uint32_t rec, int sub, int i, int lane, const Values& v, const uint32_t (&w)[N][2]) {
     const uint4 x = lds16(rec + S * D + sub * D * 16 + i * 512 + lane * 16);
     const uint32_t xw[4] = {x.x & v.there, x.y & v.there, x.z & v.there, x.w & v.there};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t a0 = mul_h2(e4m3_pair(xw[2 * h]), v.u0), a2 = mul_h2(e4m3_pair(xw[2 * h] >> 16), v.u1);
       const uint32_t a1 = mul_h2(e4m3_pair(xw[2 * h + 1]), v.u0), a3 = mul_h2(e4m3_pair(xw[2 * h + 1] >> 16), v.u1);
-      mma_f16_16816(acc[2 * i + h], a0, a1, a2, a3, hi[0], hi[1]);
-      mma_f16_16816(acc[2 * i + h], a0, a1, a2, a3, lo[0], lo[1]);
+#pragma unroll
+      for (int n = 0; n < N; ++n) mma_f16_16816(acc[2 * i + h], a0, a1, a2, a3, w[n][0], w[n][1]);
     }
   }
 
@@ -152,21 +152,25 @@ template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
     const Values v0 = values(rec0, sub0, tok0, rq.held, lane);
     Values v1{};
     if (two) v1 = values(rec1, sub1, tok1, rq.held, lane);
-    uint32_t hi0[2], lo0[2], hi1[2] = {0u, 0u}, lo1[2] = {0u, 0u};
     if constexpr (PACK) {
       const bool second = lane & 2;
       const uint32_t scales = (second && two ? rec1 + 16 * sub1 : rec0 + 16 * sub0) + 2 * S * D + g;
       const float fa = scale_f(lds1(scales)), fb = scale_f(lds1(scales + 8));
       const float s[4] = {(second ? s1[0] : s0[0]) * fa, (second ? s1[1] : s0[1]) * fa,
                           (second ? s1[2] : s0[2]) * fb, (second ? s1[3] : s0[3]) * fb};
+      uint32_t hi[2], lo[2], w0[1][2], w1[1][2];
       // without a second group its columns see nothing
-      Base::weigh(a, rq, second ? (two ? tok1 : rq.hi) : tok0, s, scale2, lane, hi0, lo0);
+      Base::template weigh<true>(a, rq, second ? (two ? tok1 : rq.hi) : tok0, s, scale2, lane, hi, lo);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        hi1[i] = g < 4 ? 0u : hi0[i];
-        lo1[i] = g < 4 ? 0u : lo0[i];
-        hi0[i] = g < 4 ? hi0[i] : 0u;
-        lo0[i] = g < 4 ? lo0[i] : 0u;
+      for (int i = 0; i < 2; ++i) {                    // a group's lower halves to the other columns
+        const uint32_t away = __shfl_xor_sync(FULL, lo[i], 16);
+        w0[0][i] = g < 4 ? hi[i] : away;
+        w1[0][i] = g < 4 ? away : hi[i];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        add<1>(rec0, sub0, i, lane, v0, w0);
+        if (two) add<1>(rec1, sub1, i, lane, v1, w1);
       }
     } else {
       auto scaled = [&](uint32_t rec, int sub, float (&s)[4]) {
@@ -174,21 +178,22 @@ template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
         const float fa = scale_f(lds1(scales)), fb = scale_f(lds1(scales + 8));
         s[0] *= fa; s[1] *= fa; s[2] *= fb; s[3] *= fb;
       };
+      uint32_t w0[2][2], w1[2][2];
       scaled(rec0, sub0, s0);
       if (two) scaled(rec1, sub1, s1);
-      Base::weigh(a, rq, tok0, s0, scale2, lane, hi0, lo0);
+      Base::weigh(a, rq, tok0, s0, scale2, lane, w0[0], w0[1]);
       if (two) {
         // a new maximum rescales sums that the first group's products are not
         // in yet: its weights are rescaled with them
         const float m0 = m[0], m1 = m[1];
-        Base::weigh(a, rq, tok1, s1, scale2, lane, hi1, lo1);
-        if (__any_sync(FULL, m[0] != m0 || m[1] != m1)) Base::reweigh(m0, m1, lane, hi0, lo0);
+        Base::weigh(a, rq, tok1, s1, scale2, lane, w1[0], w1[1]);
+        if (__any_sync(FULL, m[0] != m0 || m[1] != m1)) Base::reweigh(m0, m1, lane, w0[0], w0[1]);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      add(rec0, sub0, i, lane, v0, hi0, lo0);
-      if (two) add(rec1, sub1, i, lane, v1, hi1, lo1);
+      for (int i = 0; i < D / 32; ++i) {
+        add<2>(rec0, sub0, i, lane, v0, w0);
+        if (two) add<2>(rec1, sub1, i, lane, v1, w1);
+      }
     }
     if ((Base::since += two ? 2 : 1) >= 8) Base::settle();
   }
@@ -212,15 +217,9 @@ template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
       Base::settle();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const float mx = fmaxf(m[c], __shfl_xor_sync(FULL, m[c], 2));
-        const float f = mx == -INFINITY ? 0.f : ex2(m[c] - mx);
-        m[c] = mx;
-        l[c] *= f;
         l[c] += __shfl_xor_sync(FULL, l[c], 2);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          sum[k][c] *= f;
-          sum[k][2 + c] *= f;
           sum[k][c] += __shfl_xor_sync(FULL, sum[k][c], 2);
           sum[k][2 + c] += __shfl_xor_sync(FULL, sum[k][2 + c], 2);
         }
