@@ -96,12 +96,14 @@ template <> struct Pack<float> {
   }
 };
 
-// Rotate the VEC pairs of two 16-byte pieces, in fp32: pair e is (x[e], x[e +
-// VEC]), or with IL the neighbours (2e, 2e + 1) of the two pieces in a row.
+// Rotate the VEC pairs held by two 16-byte vectors: pair e is (a[e], b[e]),
+// or with IL the neighbours (2e, 2e + 1) of the two vectors in a row.
 template <typename T, bool IL>
-__device__ __forceinline__ void turn_pairs(float* x, const float* cs, const float* sn) {
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float* cs, const float* sn) {
   constexpr int VEC = Elem<T>::kVec;
-  float c[VEC], s[VEC];
+  float x[2 * VEC], y[2 * VEC], c[VEC], s[VEC];
+  unpack16<T>(a, x);
+  unpack16<T>(b, x + VEC);
 #pragma unroll
   for (int e = 0; e < VEC; e += 4) {
     *reinterpret_cast<float4*>(c + e) = *reinterpret_cast<const float4*>(cs + e);
@@ -110,20 +112,11 @@ __device__ __forceinline__ void turn_pairs(float* x, const float* cs, const floa
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     const int i = IL ? 2 * e : e, j = IL ? 2 * e + 1 : e + VEC;
-    const float a = x[i], b = x[j];
-    x[i] = a * c[e] - b * s[e];
-    x[j] = b * c[e] + a * s[e];
+    y[i] = x[i] * c[e] - x[j] * s[e];
+    y[j] = x[j] * c[e] + x[i] * s[e];
   }
-}
-template <typename T, bool IL>
-__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float* cs, const float* sn) {
-  constexpr int VEC = Elem<T>::kVec;
-  float x[2 * VEC];
-  unpack16<T>(a, x);
-  unpack16<T>(b, x + VEC);
-  turn_pairs<T, IL>(x, cs, sn);
-  a = Pack<T>::pack(x);
-  b = Pack<T>::pack(x + VEC);
+  a = Pack<T>::pack(y);
+  b = Pack<T>::pack(y + VEC);
 }
 
 // Stored min/max of one 16-byte piece of dims as order-preserving keys, and
@@ -180,22 +173,6 @@ struct Box {
     }
   }
 };
-
-// Physical page of logical page lp of request r, or -1 (reported) where the
-// table or the pool has none. For the whole CTA.
-__device__ __forceinline__ int page_of(const RopeAppendArgs& a, int r, int lp) {
-  const int entry = a.page_indptr[r] + lp;
-  if (lp >= a.page_indptr[r + 1] - a.page_indptr[r] || entry >= a.nnz) {
-    if (threadIdx.x == 0) report(a.err, QUEST_DEVERR_TABLE_RANGE);
-    return -1;
-  }
-  const int pp = a.page_indices[entry];
-  if (pp < 0 || pp >= a.n_phys) {
-    if (threadIdx.x == 0) report(a.err, QUEST_DEVERR_PAGE_RANGE);
-    return -1;
-  }
-  return pp;
-}
 
 // A lane's two pieces of a row, at tokens tg, tg + TG, ...: the loads of four
 // tokens are in flight before the first is used, then `each` handles them and

@@ -108,7 +108,7 @@ struct Logit {
 template <typename Sh>
 __device__ __forceinline__ void copy_boxes(const DecodeMaps& maps, const DenseArgs& a, int id, int g, int slot,
                                            uint32_t dst, uint64_t* bar, uint64_t pol) {
-  const int y = (id * a.h_kv + g) * a.page_size + slot;
+  const int y = ((id * a.h_kv + g) << (a.page_size == 16 ? 4 : 5)) + slot;
 #pragma unroll
   for (int b = 0; b < Sh::BOXES; ++b) {
     tma_2d_hint(dst + b * Sh::BOX, &maps.k, b * Sh::COLS, y, smem_u32(bar), pol);
@@ -589,7 +589,7 @@ dense_decode_kernel(const __grid_constant__ typename W::Source source, const Dec
     const int lp = LIST ? __shfl_sync(FULL, pages, at - ids_at) : rq.tile0 + at;
     const bool none = LIST && lp < 0, bad = none || id < 0 || id >= a.n_phys;
     if (lane == 0) {
-      s_meta[warp][st] = make_int4(r, g, at, bad ? -1 : lp * TT);
+      s_meta[warp][st] = make_int4(r, g, at, bad ? -1 : LIST ? lp * TT : 0);   // w: no page, or a list's token
       if (!bad) {
         uint64_t* bar = &s_bar[warp][st];
         mbar_expect_tx(bar, Sh::STAGE + (fault && st == 0 ? 16 : 0));
@@ -656,7 +656,7 @@ dense_decode_kernel(const __grid_constant__ typename W::Source source, const Dec
     if (meta.w >= 0) {
       if (!warp_wait_bounded(&s_bar[warp][st], phase >> st & 1, p.wait_limit)) { ok = false; break; }
       phase ^= 1u << st;
-      w.tile(a, cq, meta.w, ring + st * Sh::STAGE, s_q[QS ? warp : 0], scale2, lane);
+      w.tile(a, cq, LIST ? meta.w : (cq.tile0 + meta.z) * TT, ring + st * Sh::STAGE, s_q[QS ? warp : 0], scale2, lane);
     }
     __syncwarp();
     if (done + NST < total) issue(st);

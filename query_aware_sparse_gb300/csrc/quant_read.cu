@@ -6,6 +6,10 @@
 // Split. A warp takes one page of one KV head: 16 bytes per lane and load, as
 // the record lays them out (e4m3_page.cuh), K's as 32 bytes of one token, V's as
 // 8 bytes of four tokens, which eight lanes make 64 bytes of a row.
+//
+// Measured: 65536 tokens of 8 heads (128 dims) 68 us, 5920 GB/s (88% of the rate of
+// a copy, which writes as much as it reads; here two thirds are writes). V in 16
+// bytes of two tokens, traded between lanes: 71 us; CTAs of four warps: 68.
 #include "e4m3_page.cuh"
 #include "dense.cuh"
 #include "quant.h"

@@ -58,7 +58,18 @@ __global__ void __launch_bounds__(NT, 512 / NT) rope_append_kernel(const RopeApp
     s_sin[t * (D / 2) + jj] = sn;
   }
 
-  const int pp = page_of(a, r, lp);             // without a page the queries are rotated all the same
+  // the page; without one the queries are rotated all the same
+  const int entry = a.page_indptr[r] + lp;
+  int pp = -1;
+  if (lp >= a.page_indptr[r + 1] - a.page_indptr[r] || entry >= a.nnz) {
+    if (threadIdx.x == 0) report(a.err, QUEST_DEVERR_TABLE_RANGE);
+  } else {
+    pp = a.page_indices[entry];
+    if (pp < 0 || pp >= a.n_phys) {
+      if (threadIdx.x == 0) report(a.err, QUEST_DEVERR_PAGE_RANGE);
+      pp = -1;
+    }
+  }
   __syncthreads();
 
   const int h0 = blockIdx.y * a.heads_per_cta, h1 = min(a.h_kv, h0 + a.heads_per_cta);

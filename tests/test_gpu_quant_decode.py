@@ -149,19 +149,31 @@ def test_scales_of_every_size():
     assert qs.device_error() == 0
 
 
-def test_large_scores():
-    """Logits of several hundred, rising along the cache."""
+@pytest.mark.parametrize("d,S,group", [(64, 16, 2), (64, 32, 8), (128, 32, 8), (128, 32, 4), (64, 32, 1)])
+def test_large_scores(d, S, group):
+    """Logits of several hundred, rising token by token: the running maximum
+    moves all the time, inside a page too, and nothing overflows."""
     from tests._cases import random_case
-    case = random_case(61, [3000, 700], h_kv=2, group=2, d=64, S=16)
+    case = random_case(61, [3000, 700], h_kv=2, group=group, d=d, S=S)
     case["q"] = (case["q"] * 0 + 8).half()
     t = case["table"]
     for r, L in enumerate(t.seq_lens):
-        for p in range(-(-int(L) // 16)):
+        for p in range(-(-int(L) // S)):
             x = case["k_pool"][t.page_indices[t.page_indptr[r] + p]]
-            x[~x.isnan()] = (p - 90) * 0.03
+            rise = (torch.arange(S)[:, None] + p * S - 1440) * (0.12 / 64)
+            x[~x.isnan()] = rise.half().expand_as(x)[~x.isnan()]
     requantise(case)
     _dense(case)
     _sparse(case, 40)
+
+
+@pytest.mark.parametrize("d,S,group", [(128, 32, 8), (64, 32, 8), (128, 16, 8), (64, 16, 1), (64, 32, 4)])
+def test_equal_runs(d, S, group):
+    """Tables and lists that are too long for a cluster per unit, with masks."""
+    case = quant_case(330 + S + group, [24000, 31, 0, 9000], h_kv=1, group=group, d=d, S=S)
+    _dense(case)
+    _dense(case, ["cap", "alibi", "doc"], seed=3)
+    _sparse(case, 700, seed=1, drop=0.1)
 
 
 def test_bad_pages_are_skipped_and_reported():
@@ -325,6 +337,20 @@ def test_without_lse_and_with_a_scale():
                                                 out.data_ptr(), None, ctypes.c_float(0.31), ws.data_ptr(), ws.numel(),
                                                 torch.cuda.current_stream().cuda_stream)
     assert st == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("d,group", [(128, 2), (64, 8)])
+def test_wait_runs_out_in_the_equal_runs(d, group):
+    """Calls that are too long for a cluster per unit."""
+    import query_aware_sparse_gb300 as qs
+    case = quant_case(202, [20000, 300], h_kv=1, group=group, d=d, S=16)
+    cache, t, q = gpu_quant(case), gpu_table(case["table"]), case["q"].cuda()
+    _recovers(lambda: qs.quant_dense_decode_attn(cache, t, q, group),
+              lambda o, l: check_attention(np_of(o), np_of(l), _reference(case), 0.0, 0.0, 20000))
+    sel, phys = _lists(case, 1000, 7)
+    dev = dev_i32(sel), dev_i32(phys)
+    _recovers(lambda: qs.quant_sparse_decode_attn(cache, t, q, group, *dev, 1000),
+              lambda o, l: check_attention(np_of(o), np_of(l), _sparse_reference(case, sel), 0.0, 0.0, 16000))
 
 
 @pytest.mark.parametrize("d,group", [(128, 2), (64, 8)])
