@@ -643,9 +643,10 @@ QUEST_API quest_status quest_quant_read_kv(const quest_quant_cache* cache,
 /*
  * quest_quant_sparse_decode_attn — quest_sparse_decode_attn over a
  * quest_quant_cache: the same lists, results and errors, fp32 accuracy against
- * the stored numbers. The slots of all lists are cut into equal runs, one per
- * warp; the parts of a list that is cut over several runs are joined by
- * log-sum-exp in a second kernel, always in the same order.
+ * the stored numbers. Short lists go to a cluster each (one launch), the slots of
+ * many long ones are cut into equal runs, one per warp, as in
+ * quest_dense_decode_attn; parts are joined by log-sum-exp, always in the same
+ * order.
  *   q         : device fp16 [batch, h_kv * group, head_dim]
  *   out       : device fp32, 16-byte aligned
  *   workspace : device, >= quest_quant_decode_workspace_size(...) bytes, 16-B

@@ -118,6 +118,52 @@ def test_e4m3_summaries(d, S):
     _check(5, LENS, BEFORE, d=d, S=S, fp8=True)
 
 
+def _as_they_are(x, S=16, fp8=False):
+    """x [n, h, d] as keys that are neither normed nor rotated, a request each."""
+    import query_aware_sparse_gb300 as qs
+    n, h, d = x.shape
+    cache = qs.PagedCache.empty(n, h, S, d, F16, summary_fp8=fp8)
+    table = qs.PageTable(dev_i32(np.arange(n + 1)), dev_i32(np.arange(n)), dev_i32(np.ones(n)))
+    k = torch.from_numpy(x).cuda()
+    qs.norm_rope_append_kv(cache, table, None, k, k, dev_i32(np.arange(n + 1)), dev_i32(np.zeros(n)), qs.QKNorm(None, None), 1)
+    assert np.array_equal(_bits(np_of(cache.k_pool)[:, :, 0]), _bits(x))
+    return np_of(cache.summary)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_e4m3_summary_of_every_fp16_number(d):
+    """Pages of one token each: the box of a number is its floor and its ceiling."""
+    import query_aware_sparse_gb300 as qs
+    bits = np.arange(1 << 16, dtype=np.uint16)
+    bits = bits[bits & 0x7c00 != 0x7c00]
+    x = bits.view(np.float16).reshape(-1, 1, d)
+    got = _as_they_are(x, fp8=True)
+    assert qs.device_error() == 0x10
+    assert np.array_equal(got, qo.summary_to_e4m3(np.stack([x, x], 2))[0])
+    small = x[(np.abs(x) <= 448).all(-1)[:, 0]]
+    _as_they_are(np.ascontiguousarray(small), fp8=True)
+    assert qs.device_error() == 0
+
+
+def test_zeros_keep_their_order():
+    """-0 below +0, in fp16 boxes as in fp32 ones."""
+    for dtype in (F16, F32):
+        for d, S in ((128, 16), (64, 32)):
+            import query_aware_sparse_gb300 as qs
+            rng = np.random.default_rng(1)
+            x = np.where(rng.random((S, 2, d)) < 0.5, 0.0, -0.0).astype(np.float16 if dtype == F16 else np.float32)
+            x[:3] = rng.normal(size=(3, 2, d)) * (rng.random((3, 2, d)) < 0.3)
+            cache = qs.PagedCache.empty(1, 2, S, d, dtype)
+            table = qs.PageTable(dev_i32([0, 1]), dev_i32([0]), dev_i32([S]))
+            k = torch.from_numpy(x).cuda()
+            for a, b in ((0, 5), (5, S)):
+                qs.norm_rope_append_kv(cache, table, None, k[a:b], k[a:b], dev_i32([0, b - a]), dev_i32([a]),
+                                       qs.QKNorm(None, None), 1)
+            okp, ovp, osm = (np.zeros(t.shape, x.dtype) for t in (cache.k_pool, cache.v_pool, cache.summary))
+            qo.append_kv(okp, ovp, osm, np.array([0, 1]), np.array([0]), np.zeros(1, np.int32), np.array([0, S]), x, x)
+            assert np.array_equal(_bits(np_of(cache.summary)), _bits(osm))
+
+
 def test_one_token_and_batches():
     _check(6, [1], [0], h=1, group=1)
     rng = np.random.default_rng(1)

@@ -154,6 +154,7 @@ def test_what_cannot_be_kept_is_reported():
     fine = torch.randn((20, 2, 128), generator=torch.Generator().manual_seed(5)).half()
     _check(12, [20], [9], k=x.cuda(), v=fine.cuda(), error=FP8_RANGE)
     _check(13, [20], [9], k=fine.cuda(), v=x.cuda(), error=FP8_RANGE)
+    _check(16, [20], [9], k=(fine * 300).cuda(), v=fine.cuda(), fp8=True, error=FP8_RANGE)   # beyond the summary's range
     fine[0, 0, 0] = 57344.0
     _check(14, [20], [9], k=fine.cuda(), v=fine.cuda())
 
