@@ -202,13 +202,12 @@ __device__ __forceinline__ void walk_rows(const T* src, int64_t src_stride, T* d
 // CTAs of an append: (request, touched page) by KV heads; sets heads_per_cta.
 // A request with n new tokens touches at most ceil(n / S) + 1 pages, each with
 // one token at least. Few pages: the KV heads of one are spread over CTAs until
-// every SM has one; more CTAs only start more often (200 one-token requests of 8
-// KV heads: 9.5 us with 152 CTAs wanted, 13.6 with 608; 2048 tokens 11.5 and 19.3).
-inline dim3 append_grid(RopeAppendArgs& a, int sms) {
+// there are `wanted`.
+inline dim3 append_grid(RopeAppendArgs& a, long long wanted) {
   long long segs = (long long)(a.n_new + a.page_size - 1) / a.page_size + 2LL * a.batch;
   if (segs > a.n_new) segs = a.n_new;
   a.heads_per_cta = a.h_kv;
-  while (a.heads_per_cta > 1 && segs * ((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta) < sms)
+  while (a.heads_per_cta > 1 && segs * ((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta) < wanted)
     a.heads_per_cta = (a.heads_per_cta + 1) / 2;
   return dim3((unsigned)segs, (unsigned)((a.h_kv + a.heads_per_cta - 1) / a.heads_per_cta));
 }

@@ -8,7 +8,13 @@ namespace quest {
 cudaError_t launch_norm_append(const NormAppendArgs& args, bool e4m3, cudaStream_t s) {
   NormAppendArgs p = args;
   const int sms = sm_count();
-  const dim3 grid = append_grid(p.a, sms);
+  // A CTA per SM, as in rope_append.cu; with more work than that (over 12 steps
+  // of 4 KB for each of the 16 warps that an SM holds) five, so that the last ones
+  // are short: 3300 tokens of 32 heads of 8, 64 dims, 66 -> 59 us, 14400 fp32
+  // tokens of 8 heads of 2 88 -> 80; but 2048 tokens of 8 heads of 4 15 -> 17.
+  const long long row = (long long)p.a.head_dim * (p.a.dtype == QUEST_F16 ? 2 : 4);
+  const long long rows = (long long)p.a.h_kv * ((p.a.q ? p.a.group : 0) + 2) * p.a.n_new;
+  const dim3 grid = append_grid(p.a, rows * row / 4096 > 12LL * 16 * sms ? 5LL * sms : sms);
   if (e4m3) return launch_norm_append_e4m3(p, grid, sms, s);
   return p.a.dtype == QUEST_F16 ? launch_norm_append_f16(p, grid, sms, s) : launch_norm_append_f32(p, grid, sms, s);
 }

@@ -17,18 +17,18 @@
 // the 16-byte chunks of the record; where the page is not complete each token's
 // bytes are stored by themselves (a code's byte belongs to one token).
 //
-// Bound: HBM for prompts, if the warps' arithmetic keeps out of the way: with two
-// CTAs of eight warps per SM (registers) a row's chain norm - rotate - quantise
+// Bound: HBM for prompts, if the warps' arithmetic keeps out of the way: with 16
+// warps per SM (registers) a row's chain norm - rotate - quantise
 // is as long as its copy. So the next step's rows are fetched while one is
 // treated, the tokens of a step are treated side by side, pairs in packed fp32,
 // boxes as fp16 minima and maxima, not as ordered keys. Decode steps: latency.
 //
-// Measured: 65536 tokens, 8 KV heads of 4, normed, fp16 with E4M3 summaries 267
-// us, 6040 GB/s (89% of the copy rate; 357 with loads, chain and stores in turn,
-// 325 with the next step fetched, 278 with a step's tokens side by side);
-// 131072 tokens of 32 heads into E4M3, pages of 32, 835 us, 6520 GB/s (96%;
-// 1196 with spills, which max.NaN on magnitudes ended). Three steps held instead
-// of two: 283 and 896 us. One token of 16 requests, 8 KV heads of 4: 4.3 us, into
+// Measured: 65536 tokens, 8 KV heads of 4, normed, fp16 with E4M3 summaries 248
+// us, 6500 GB/s (96% of the copy rate; 357 with loads, chain and stores in turn,
+// 325 with the next step fetched, 278 with a step's tokens side by side, 267 with
+// fp16 boxes); 131072 tokens of 32 heads into E4M3, pages of 32, 826 us, 6590 GB/s
+// (97%; 1196 with spills, which max.NaN on magnitudes ended). Three steps held
+// instead of two: 283 instead of 267, 896 instead of 835. One token of 16 requests, 8 KV heads of 4: 4.3 us, into
 // E4M3 5.1.
 #pragma once
 
@@ -607,13 +607,13 @@ cudaError_t launch_norm_append_n(const NormAppendArgs& p, dim3 grid, cudaStream_
   kernel<<<grid, NT, smem, s>>>(p);
   return cudaGetLastError();
 }
-// Four warps per CTA for many CTAs of few rows, as in rope_append.cu.
+// Many CTAs: four warps each, four of them per SM, whose starts the others hide
+// (65536 tokens, 8 KV heads of 4: 267 us with eight warps, 248 with four). Where
+// the device is not full eight warps get through a page sooner.
 template <typename T, int D, bool E4, bool F8>
 cudaError_t launch_norm_append_t(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s) {
-  const int rows = p.a.heads_per_cta * ((p.a.q ? p.a.group : 0) + 2);
-  const bool small = rows <= 16 && (long long)grid.x * grid.y > 4LL * sms;
-  return small ? launch_norm_append_n<T, D, E4, F8, 128>(p, grid, s)
-               : launch_norm_append_n<T, D, E4, F8, 256>(p, grid, s);
+  return (long long)grid.x * grid.y > 4LL * sms ? launch_norm_append_n<T, D, E4, F8, 128>(p, grid, s)
+                                                : launch_norm_append_n<T, D, E4, F8, 256>(p, grid, s);
 }
 
 }  // namespace quest

@@ -169,6 +169,8 @@ cudaError_t launch(const RopeAppendArgs& a, dim3 grid, int sms, cudaStream_t s) 
 cudaError_t launch_rope_append(const RopeAppendArgs& args, cudaStream_t s) {
   RopeAppendArgs a = args;
   const int sms = sm_count();
+  // a CTA per SM; more of them only start more often (200 one-token requests of 8
+  // KV heads: 9.5 us with 152 CTAs wanted, 13.6 with 608; 2048 tokens 11.5 and 19.3)
   const dim3 grid = append_grid(a, sms);
   if (a.dtype == QUEST_F16 && a.summary_fp8)
     return a.head_dim == 128 ? launch<__half, 128, true>(a, grid, sms, s) : launch<__half, 64, true>(a, grid, sms, s);
