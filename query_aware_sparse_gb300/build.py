@@ -26,8 +26,9 @@ SOURCES = ["quest_api.cu", "append.cu", "score.cu", "select.cu", "attn.cu", "ste
            "dense_api.cu", "rope_append.cu", "dense_decode.cu", "prefill.cu",
            "prefill_f16_d64_t1.cu", "prefill_f16_d64_t2.cu", "prefill_f16_d128_t1.cu",
            "prefill_f16_d128_t2.cu", "prefill_f32.cu",
-           "quant_api.cu", "norm_append.cu", "norm_append_f16.cu", "norm_append_f32.cu",
-           "norm_append_e4m3.cu", "quant_read.cu", "quant_decode.cu"]
+           "quant_api.cu", "norm_append.cu", "norm_append_f16_d64.cu", "norm_append_f16_d128.cu",
+           "norm_append_f32.cu", "norm_append_e4m3_d64.cu", "norm_append_e4m3_d128.cu",
+           "quant_read.cu", "quant_decode.cu"]
 SHARED_HEADERS = ("common.cuh", "internal.h")
 STEP_HEADERS = ("topk.cuh", "attn_dev.cuh", "attn_mma.cuh", "step_impl.cuh", "cstep_impl.cuh")
 DENSE_HEADERS = ("dense.h", "dense.cuh", "tc.cuh", "tmap.h",

@@ -17,6 +17,9 @@
 // the workspace, at place (warp + unit): the two only ever grow along the
 // runs, so no two parts meet there. A second kernel joins them in run order.
 //
+// The kernel also serves the E4M3 cache (quant_decode.cuh), whose tiles are pages,
+// and, with LIST, pages that a list names instead of the page table.
+//
 // fp16 on mma.sync m16n8k16, keys and dims as the 16 rows, the group's heads
 // as (up to) the 8 columns:  S^T = K Q^T,  O^T += V^T P^T.  P is passed as two
 // fp16 numbers, p = p1 + p2 to 2^-22, so the output keeps fp32 accuracy.
@@ -674,8 +677,8 @@ dense_decode_kernel(const __grid_constant__ typename W::Source source, const Dec
 }
 
 // Joins the parts of one (request, query head): the threads take the parts'
-// maxima and sums and leave each part's weight in shared memory, then the warps
-// their share of the parts' o (loads without anything to wait for), whose sums meet
+// maxima and sums and leave each part's weight in shared memory, then each warp
+// its share of the parts' o (loads without anything to wait for), whose sums meet
 // in shared memory, in a fixed order.
 constexpr int kJoinThreads = 256;
 template <int D, int NT = kJoinThreads>

@@ -1,4 +1,4 @@
-// Normed and E4M3 appends: launch (norm_append.cuh, one file per store).
+// Normed and E4M3 appends: launch (norm_append.cuh, one file per store and head dim).
 #include "append_parts.cuh"
 #include "quant.h"
 #include "tmap.h"
@@ -15,8 +15,10 @@ cudaError_t launch_norm_append(const NormAppendArgs& args, bool e4m3, cudaStream
   const long long row = (long long)p.a.head_dim * (p.a.dtype == QUEST_F16 ? 2 : 4);
   const long long rows = (long long)p.a.h_kv * ((p.a.q ? p.a.group : 0) + 2) * p.a.n_new;
   const dim3 grid = append_grid(p.a, rows * row / 4096 > 12LL * 16 * sms ? 5LL * sms : sms);
-  if (e4m3) return launch_norm_append_e4m3(p, grid, sms, s);
-  return p.a.dtype == QUEST_F16 ? launch_norm_append_f16(p, grid, sms, s) : launch_norm_append_f32(p, grid, sms, s);
+  const bool d128 = p.a.head_dim == 128;
+  if (e4m3) return d128 ? launch_norm_append_e4m3_d128(p, grid, sms, s) : launch_norm_append_e4m3_d64(p, grid, sms, s);
+  if (p.a.dtype == QUEST_F32) return launch_norm_append_f32(p, grid, sms, s);
+  return d128 ? launch_norm_append_f16_d128(p, grid, sms, s) : launch_norm_append_f16_d64(p, grid, sms, s);
 }
 
 }  // namespace quest

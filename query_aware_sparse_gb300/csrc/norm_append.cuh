@@ -28,8 +28,8 @@
 // 325 with the next step fetched, 278 with a step's tokens side by side, 267 with
 // fp16 boxes); 131072 tokens of 32 heads into E4M3, pages of 32, 826 us, 6590 GB/s
 // (97%; 1196 with spills, which max.NaN on magnitudes ended). Three steps held
-// instead of two: 283 instead of 267, 896 instead of 835. One token of 16 requests, 8 KV heads of 4: 4.3 us, into
-// E4M3 5.1.
+// instead of two: 283 instead of 267, 896 instead of 835. One token of 16 requests, 8 KV heads of 4: 3.5 us, into
+// E4M3 4.1.
 #pragma once
 
 #include "append_parts.cuh"
@@ -286,22 +286,23 @@ template <> struct Bounds<__half> {
 };
 
 // A row of a CTA's work is the tokens of one head, a step of it 16 tokens (fp32,
-// 128 dims: 8). A warp's next step is always on its way to shared memory while
-// it treats the one before. A lane reads back what it fetched itself, so nothing
-// but its own copies is waited for.
-template <typename T, int D> struct AppendStep {
+// 128 dims: 8), or with FEW (calls of a few tokens per request) no more than
+// stand side by side. A warp's next step is always on its way to shared memory
+// while it treats the one before. A lane reads back what it fetched itself, so
+// nothing but its own copies is waited for.
+template <typename T, int D, bool E4, bool FEW> struct AppendStep {
   static constexpr int PC = D * sizeof(T) / 32; // lanes per token: pairs of 16-byte pieces
   static constexpr int TG = 32 / PC;            // tokens side by side
-  static constexpr int U = TG < 8 ? 4 : 2;      // and one after the other
-  static constexpr uint32_t BYTES = U * 1024;
-  static constexpr int HELD = U == 2 ? 3 : 2;   // steps in shared memory per warp
+  static constexpr int U = FEW ? 1 : TG < 8 ? 4 : 2;   // and one after the other
+  static constexpr uint32_t BYTES = E4 ? 16 * D * 2 : U * 1024;   // (E4M3 values: always 16 tokens)
+  static constexpr int HELD = BYTES < 4096 ? 3 : 2;    // steps in shared memory per warp
 };
 
-template <typename T, int D, bool E4, bool F8, bool IL, int NT>
+template <typename T, int D, bool E4, bool F8, bool IL, bool FEW, int NT>
 __global__ void __launch_bounds__(NT, 512 / NT) norm_append_kernel(const NormAppendArgs p) {
   static_assert(sizeof(T) == 2 || !(E4 || F8), "8-bit codes are made of fp16 rows");
   constexpr int VEC = Elem<T>::kVec;
-  using Step = AppendStep<T, D>;
+  using Step = AppendStep<T, D, E4, FEW>;
   constexpr int PC = Step::PC, TG = Step::TG, U = Step::U, NW = NT / 32;
   extern __shared__ __align__(16) uint8_t s_fetch[];
   __shared__ __align__(16) float s_cos[kMaxPage * D / 2], s_sin[kMaxPage * D / 2];
@@ -598,22 +599,31 @@ __global__ void __launch_bounds__(NT, 512 / NT) norm_append_kernel(const NormApp
   if ((E4 || F8) && ovf) report(a.err, QUEST_DEVERR_FP8_RANGE);
 }
 
-template <typename T, int D, bool E4, bool F8, int NT>
+template <typename T, int D, bool E4, bool F8, bool FEW, int NT>
 cudaError_t launch_norm_append_n(const NormAppendArgs& p, dim3 grid, cudaStream_t s) {
-  constexpr int smem = NT / 32 * AppendStep<T, D>::HELD * AppendStep<T, D>::BYTES;
-  auto kernel = p.a.interleaved ? norm_append_kernel<T, D, E4, F8, true, NT> : norm_append_kernel<T, D, E4, F8, false, NT>;
+  using Step = AppendStep<T, D, E4, FEW>;
+  constexpr int smem = NT / 32 * Step::HELD * Step::BYTES;
+  auto kernel = p.a.interleaved ? norm_append_kernel<T, D, E4, F8, true, FEW, NT>
+                                : norm_append_kernel<T, D, E4, F8, false, FEW, NT>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, NT, smem, s>>>(p);
   return cudaGetLastError();
 }
-// Many CTAs: four warps each, four of them per SM, whose starts the others hide
-// (65536 tokens, 8 KV heads of 4: 267 us with eight warps, 248 with four). Where
-// the device is not full eight warps get through a page sooner.
+// Up to four new tokens per request, on average: a step goes through no more of
+// them than stand side by side (a token of 16 requests 4.3 -> 3.5 us, of 200
+// requests 15 -> 9; a branch inside one kernel made it too large: 65536 tokens
+// 248 -> 260). Many CTAs: four warps each, four of them per SM, whose starts the
+// others hide (65536 tokens, 8 KV heads of 4: 267 us with eight warps, 248 with
+// four). Where the device is not full eight warps get through a page sooner.
 template <typename T, int D, bool E4, bool F8>
 cudaError_t launch_norm_append_t(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s) {
-  return (long long)grid.x * grid.y > 4LL * sms ? launch_norm_append_n<T, D, E4, F8, 128>(p, grid, s)
-                                                : launch_norm_append_n<T, D, E4, F8, 256>(p, grid, s);
+  const bool many = (long long)grid.x * grid.y > 4LL * sms;
+  if (p.a.n_new <= 4LL * p.a.batch)
+    return many ? launch_norm_append_n<T, D, E4, F8, true, 128>(p, grid, s)
+                : launch_norm_append_n<T, D, E4, F8, true, 256>(p, grid, s);
+  return many ? launch_norm_append_n<T, D, E4, F8, false, 128>(p, grid, s)
+              : launch_norm_append_n<T, D, E4, F8, false, 256>(p, grid, s);
 }
 
 }  // namespace quest

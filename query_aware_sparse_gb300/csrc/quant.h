@@ -1,5 +1,5 @@
 // Host-side interfaces of the normed append and of the E4M3 cache: append
-// (norm_append_*.cu), read-back (quant_read.cu) and decode attention
+// (norm_append*.cu), read-back (quant_read.cu) and decode attention
 // (quant_decode.cu), behind quant_api.cu.
 #pragma once
 
@@ -16,10 +16,15 @@ struct NormAppendArgs {
   float eps;
 };
 cudaError_t launch_norm_append(const NormAppendArgs& p, bool e4m3, cudaStream_t s);
-// Per store and element type (norm_append_<name>.cu).
-cudaError_t launch_norm_append_e4m3(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s);
-cudaError_t launch_norm_append_f16(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s);
-cudaError_t launch_norm_append_f32(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s);
+// Per store, element type and head dim (norm_append_<name>.cu).
+#define QUEST_NORM_APPEND(name) \
+  cudaError_t launch_norm_append_##name(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s);
+QUEST_NORM_APPEND(e4m3_d64)
+QUEST_NORM_APPEND(e4m3_d128)
+QUEST_NORM_APPEND(f16_d64)
+QUEST_NORM_APPEND(f16_d128)
+QUEST_NORM_APPEND(f32)
+#undef QUEST_NORM_APPEND
 
 struct QuantReadArgs {
   const uint8_t* pool; void* k_out; void* v_out;

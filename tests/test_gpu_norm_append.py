@@ -172,6 +172,14 @@ def test_one_token_and_batches():
     _check(9, rng.integers(0, 3, 800).tolist(), rng.integers(0, 40, 800).tolist(), h=1, group=2, d=64)
 
 
+@pytest.mark.parametrize("dtype,d,S", [(F16, 128, 16), (F16, 64, 32), (F16, 128, 32), (F32, 128, 16), (F32, 64, 32)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_long_request_among_many_without_tokens(dtype, d, S, fp8):
+    """Few tokens per request on average, and pages full of them all the same."""
+    if dtype == F16 or not fp8:
+        _check(14, [50] + [0] * 20 + [3, 1], [5] + [9] * 20 + [15, 16], d=d, S=S, dtype=dtype, fp8=fp8, interleaved=fp8)
+
+
 def test_positions():
     rng = np.random.default_rng(2)
     p = rng.integers(-2 ** 31, 2 ** 31, sum(LENS))

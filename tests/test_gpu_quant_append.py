@@ -113,6 +113,11 @@ def test_one_token_and_batches():
     _check(9, LENS, BEFORE, rope=True, with_q=False)
 
 
+@pytest.mark.parametrize("d,S", [(128, 16), (64, 32), (64, 16), (128, 32)])
+def test_a_long_request_among_many_without_tokens(d, S):
+    _check(17, [50] + [0] * 20 + [3, 1], [5] + [9] * 20 + [15, 16], d=d, S=S, norm=True, rope=True)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_magnitude(d):
     """Rows whose largest element runs through the fp16 numbers around each
