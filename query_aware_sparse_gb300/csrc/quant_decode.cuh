@@ -19,7 +19,7 @@
 // in front of the same loads, by code that is cold.
 //
 // Measured: 16 requests of 8192 to 131072 tokens, 8 KV heads of 4 (128 dims),
-// 337 us, 6820 GB/s (100% of the copy rate); 256 pages of each 25 us (72%); 128 of
+// 337 to 344 us, 6820 to 6680 GB/s (98% of the copy rate and more); 256 pages of each 25 us (72%); 128 of
 // 2048 pages of 32 heads 7.7 us; 1000 tokens of one head 4.1 us.
 #pragma once
 
@@ -329,6 +329,7 @@ quant_unit_kernel(const PageRecords source, const DecodeArgs p) {
   const uint32_t smem = smem_u32(unit_smem), ring = smem + warp * Sh::RING;
   if (lane < NST) mbar_init(&s_bar[warp][lane], 1);
   fence_mbar_init();
+  __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
 
@@ -405,6 +406,10 @@ quant_unit_kernel(const PageRecords source, const DecodeArgs p) {
       warp_wait_bounded(&s_bar[warp][st], phase >> st & 1, p.wait_limit);
   }
 
+  auto meet = [] {                                     // every CTA of the cluster, whole warps
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  };
   // the warp's part into its ring, the CTA's behind the first warp's
   auto o_at = [&](uint32_t part, int h) { return part + h * D * 4; };
   auto ml_at = [&](uint32_t part, int h) { return part + G * D * 4 + h * 8; };
@@ -438,7 +443,7 @@ quant_unit_kernel(const PageRecords source, const DecodeArgs p) {
     }
   }
   if (ctas == 1) return;
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  meet();
   for (int i = rank * kUnitWarps * 32 + threadIdx.x; i < items; i += ctas * kUnitWarps * 32) {
     const int h = i / (D / 4), d4 = i % (D / 4);
     float m, l;
@@ -448,7 +453,7 @@ quant_unit_kernel(const PageRecords source, const DecodeArgs p) {
     put(h, d4, m, l, o);
   }
   // a CTA's part stays until every other has read it
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  meet();
 }
 
 }  // namespace quest
