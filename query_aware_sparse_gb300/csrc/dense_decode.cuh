@@ -47,7 +47,7 @@ struct DecodeArgs {
   // [batch, h_kv, sel_k] logical and physical page, -1 = no page
   const int32_t* sel_logical; const int32_t* sel_phys;
   int32_t sel_k;
-  int32_t min_run;          // tiles of a run, at least
+  int32_t min_run;          // tiles of a run, at least: 4 (as a constant, E4M3 ragged batch 343 -> 346 us)
   long long* starts;        // [batch + 1] tiles before each request, all KV heads
   float* part_o;            // [warps + units, G, D]
   float2* part_ml;          // [warps + units, G]
@@ -179,25 +179,27 @@ template <int D> struct WarpMma {
     }
   }
 
-  // Products s of tokens tok0 .. tok0 + 15 -> their weights, as the two halves
-  // of P^T (k index of a half: 2 t, 2 t + 1 (+ 8)). JOINT: columns c and c + 4
-  // are of the same head and keep the same maximum.
-  template <bool JOINT = false>
-  __device__ __forceinline__ void weigh(const DenseArgs& a, const Request& rq, int tok0, const float (&s)[4],
-                                        float scale2, int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
+  // Products s(0) .. s(3) of tokens tok0 .. tok0 + 15 -> their weights, as the two
+  // halves of P^T (k index of a half: 2 t, 2 t + 1 (+ 8)). JOINT: columns c and
+  // c + 4 are of the same head and keep the same maximum. s is called where a
+  // product is used: sums of two chains taken before cost the fp16 cache 0.2 to
+  // 0.3% (ragged batch 820.4 -> 822.4 us, 32768 tokens 89.1 -> 89.4).
+  template <bool JOINT = false, typename P>
+  __device__ __forceinline__ void weigh(const DenseArgs& a, const Request& rq, int tok0, P s, float scale2,
+                                        int lane, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
     const int ta = tok0 + (lane >> 2), tb = ta + 8;
     float x[4];
     if (a.softcap > 0.f || a.slopes) {
       const float cap2 = a.softcap * LOG2E, inv = 1.f / cap2;
       const Logit f0{scale2, cap2, inv, slope2[0]}, f1{scale2, cap2, inv, slope2[1]};
       const int da = abs(rq.pos - ta), db = abs(rq.pos - tb);
-      x[0] = f0(s[0], da);
-      x[1] = f1(s[1], da);
-      x[2] = f0(s[2], db);
-      x[3] = f1(s[3], db);
+      x[0] = f0(s(0), da);
+      x[1] = f1(s(1), da);
+      x[2] = f0(s(2), db);
+      x[3] = f1(s(3), db);
     } else {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = s[c] * scale2;
+      for (int c = 0; c < 4; ++c) x[c] = s(c) * scale2;
     }
     const bool edge = tok0 < rq.lo || tok0 + 16 > rq.hi;
     if (edge) {                                        // (tok0 may be a lane's own)
@@ -297,9 +299,8 @@ template <int D> struct WarpF16 : WarpMma<D> {
         else mma_f16_16816(s0, a0, a1, a2, a3, qb[k][0], qb[k][1]);
       }
     }
-    const float s[4] = {s0[0] + s1[0], s0[1] + s1[1], s0[2] + s1[2], s0[3] + s1[3]};
     uint32_t hi[2], lo[2];
-    Base::weigh(a, rq, tok0, s, scale2, lane, hi, lo);
+    Base::weigh(a, rq, tok0, [&](int c) { return s0[c] + s1[c]; }, scale2, lane, hi, lo);
     // values of slots without a token may be anything (0 * NaN is NaN): their
     // halves of V^T are cleared. k index of a half: 2 t, 2 t + 1 (+ 8)
     uint32_t z0 = 0xffffffffu, z1 = 0xffffffffu;

@@ -171,7 +171,7 @@ template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
                           (second ? s1[2] : s0[2]) * fb, (second ? s1[3] : s0[3]) * fb};
       uint32_t hi[2], lo[2], w0[1][2], w1[1][2];
       // without a second group its columns see nothing
-      Base::template weigh<true>(a, rq, second ? (two ? tok1 : rq.hi) : tok0, s, scale2, lane, hi, lo);
+      Base::template weigh<true>(a, rq, second ? (two ? tok1 : rq.hi) : tok0, [&](int c) { return s[c]; }, scale2, lane, hi, lo);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {                    // a group's lower halves to the other columns
         const uint32_t away = __shfl_xor_sync(FULL, lo[i], 16);
@@ -192,12 +192,12 @@ template <int D, int S, bool PACK> struct WarpE4M3 : WarpMma<D> {
       uint32_t w0[2][2], w1[2][2];
       scaled(rec0, sub0, s0);
       if (two) scaled(rec1, sub1, s1);
-      Base::weigh(a, rq, tok0, s0, scale2, lane, w0[0], w0[1]);
+      Base::weigh(a, rq, tok0, [&](int c) { return s0[c]; }, scale2, lane, w0[0], w0[1]);
       if (two) {
         // a new maximum rescales sums that the first group's products are not
         // in yet: its weights are rescaled with them
         const float m0 = m[0], m1 = m[1];
-        Base::weigh(a, rq, tok1, s1, scale2, lane, w1[0], w1[1]);
+        Base::weigh(a, rq, tok1, [&](int c) { return s1[c]; }, scale2, lane, w1[0], w1[1]);
         if (__any_sync(FULL, m[0] != m0 || m[1] != m1)) Base::reweigh(m0, m1, lane, w0[0], w0[1]);
       }
 #pragma unroll
