@@ -458,6 +458,7 @@ dense_decode_kernel(const __grid_constant__ typename W::Source source, const Dec
   const uint32_t ring = ((smem_u32(smem_raw) + 1023) & ~1023u) + warp * NST * Sh::STAGE;
   if (lane < NST) mbar_init(&s_bar[warp][lane], 1);
   fence_mbar_init();
+  __syncwarp();                                        // lane 0 uses the barriers of all lanes
   pdl_wait();
 
   // Tiles of all requests before the run, and the run. A warp looks at 32
