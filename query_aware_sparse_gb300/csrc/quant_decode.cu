@@ -78,7 +78,20 @@ template <typename K> int resident_clusters(K kernel, int ctas, size_t smem, std
 //   1 head, 31 / 250 / 500 / 1000 pages          3.6 / 7.5 / 12.8 / 22     9.0 / 10.5 / 11.4 / 12.4
 //   32 heads, 125 / 250 / 500 / 1000             7.4 / 11.3 / 18 / 33      11.9 / 16.9 / 21.8 / 31.5
 //   16 requests of 8 heads, 64 / 256 / 512       10.2 / 25.2 / 45.4        16.0 / 30.5 / 50.4
-//   60 requests of 8 heads (two waves), 32 / 64 / 128   18.3 / 31.5 / 58   20.6 / 29.2 / 47.6
+// The other shapes (64 dims, pages of 32, 4 and 8 heads to a KV head) cross at the
+// same number of tiles: where the rule errs it costs 16% (64 dims, 16 requests of 8
+// heads, 1024 pages: 57.3 and 67.0 with 8 heads each, 58.7 and 63.6 with one), most
+// often under 10%.
+// More units than CTAs: the last wave is short of work and adds up to 0.6 us per
+// tile (0.4 for the smallest pages); the runs cost their 5 us and 4 ns per row of q
+// (a joining CTA each); over all shapes the border below errs by 14% at most. us for
+// lists of pages of 16, 128 dims, 1 / 8 heads to a KV head:
+//   60 requests of 8 heads, 32 pages    18.1 / 18.3    20.7 / 36.0
+//     64                                32.9 / 31.5    29.0 / 44.3
+//     128                               60.6 / 57.0    47.4 / 63.0
+//     256                               117 / 118      84.8 / 101
+//   300 requests of 8 heads, 32 pages   53.9 / 56.7    66.1 / 129
+//   1000 requests of 4 heads, 16 pages  50.5 / 55.8    61.5 / 143
 // Tables: the host knows no lengths, so all pages may be one request's, unless a
 // window bounds what is read.
 template <int D, int S, bool LIST, bool PACK> int unit_ctas(const DecodeArgs& p) {
@@ -94,7 +107,8 @@ template <int D, int S, bool LIST, bool PACK> int unit_ctas(const DecodeArgs& p)
   const int n = resident(c), sms = sm_count();
   if (n <= 0) return 0;
   const long long waves = (units + n - 1) / n, tiles = (most + kUnitWarps * c - 1) / (kUnitWarps * c);
-  return waves * tiles <= (waves > 1 ? 16 : units * c >= 2 * sms ? 64 : units * c >= sms ? 20 : 12) ? c : 0;
+  if (waves > 1) return tiles <= 12 + units * p.a.group / 150 ? c : 0;
+  return tiles <= (units * c >= 2 * sms ? 64 : units * c >= sms ? 20 : 12) ? c : 0;
 }
 
 template <int D, int S, bool LIST, bool PACK>

@@ -1,7 +1,9 @@
 """Decode over the E4M3 cache in equal runs, in the shapes whose heads stand in
 the tensor core's columns twice, against the fp64 forms on the stored numbers."""
 
+import numpy as np
 import pytest
+import torch
 
 from tests._quant_ref import quant_case
 from tests.test_gpu_quant_decode import _dense, _sparse
@@ -17,3 +19,18 @@ def test_equal_runs_of_packed_heads(d, S, group):
     _dense(case, ["cap", "alibi", "doc"], seed=3)
     _dense(case, ["window"], seed=4)
     _sparse(case, 700, seed=1, drop=0.1)
+
+
+@pytest.mark.parametrize("d,S,group", [(64, 16, 2), (128, 32, 1), (128, 16, 8)])
+def test_more_units_than_the_device_holds(d, S, group):
+    """Lists on both sides of the border between a CTA per unit, several waves of
+    them, and equal runs; some empty, some shorter than k."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(d + S)
+    batch = 3 * sms // 8 + 9                          # of 8 heads: more than three CTAs per SM
+    border = 4 * (12 + batch * 8 * group // 150)      # pages
+    lens = rng.integers(0, (border + 8) * S, batch)
+    lens[3], lens[5] = 0, (border + 8) * S
+    case = quant_case(440 + group, lens.tolist(), h_kv=8, group=group, d=d, S=S)
+    for k in (9, border, border + 1):
+        _sparse(case, k, seed=k, drop=0.1)
