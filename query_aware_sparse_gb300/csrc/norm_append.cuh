@@ -613,9 +613,12 @@ cudaError_t launch_norm_append_n(const NormAppendArgs& p, dim3 grid, cudaStream_
 // Up to four new tokens per request, on average: a step goes through no more of
 // them than stand side by side (a token of 16 requests 4.3 -> 3.5 us, of 200
 // requests 15 -> 9; a branch inside one kernel made it too large: 65536 tokens
-// 248 -> 260). Many CTAs: four warps each, four of them per SM, whose starts the
-// others hide (65536 tokens, 8 KV heads of 4: 267 us with eight warps, 248 with
-// four). Where the device is not full eight warps get through a page sooner.
+// 248 -> 260). Where one request brings a chunk this may be the slower way (250
+// requests of one token and one of 700: 18.8 us, 17.6 with full steps; 1000 and one
+// of 3000: 52 and 62): the host knows the average alone.
+// Many CTAs: four warps each, four of them per SM, whose starts the others hide
+// (65536 tokens, 8 KV heads of 4: 267 us with eight warps, 248 with four). Where the
+// device is not full eight warps get through a page sooner.
 template <typename T, int D, bool E4, bool F8>
 cudaError_t launch_norm_append_t(const NormAppendArgs& p, dim3 grid, int sms, cudaStream_t s) {
   const bool many = (long long)grid.x * grid.y > 4LL * sms;

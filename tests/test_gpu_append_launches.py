@@ -24,7 +24,7 @@ def launch(n_new, batch, h, S, d, group=0, size=2):
     """(warps of a CTA, steps of few tokens, parts of the KV heads), as chosen
     there; group 0: no queries."""
     sms = _sms()
-    much = h * (group + 2) * n_new * d * size // 4096 > 12 * 16 * sms
+    much = h * (group + 2) * n_new * d * size // 4096 > 6 * 16 * sms
     pages = min(n_new, -(-n_new // S) + 2 * batch)
     heads = h
     while heads > 1 and pages * -(-h // heads) < (5 if much else 1) * sms:
@@ -88,7 +88,7 @@ def test_plain_many_short(d, S, dtype, fp8, interleaved):
 def test_heads_in_more_parts_for_much_work():
     """Enough pages for a CTA per SM with all KV heads in one; over the limit
     of steps the heads are spread further."""
-    rows = 12 * 16 * _sms() * 4096 // 256           # of 256 bytes, just at the limit
+    rows = 6 * 16 * _sms() * 4096 // 256           # of 256 bytes, just at the limit
     for h, group in ((40, 1), (9, 8)):
         n = rows // (h * (group + 2)) + 20
         assert launch(n, 1, h, 16, 128, group) == (4, False, launch(n, 1, h, 16, 128, group)[2], True)
