@@ -472,6 +472,10 @@ typedef struct quest_score_mods {
  * page) items of all requests are cut into equal runs, one per warp, whatever
  * the requests' lengths; the parts of a unit that is cut over several runs are
  * joined by log-sum-exp in a second kernel, always in the same order.
+ * Accuracy: as with sums in fp32, but with an fp16 cache a softmax weight below
+ * 2^-9 of the row's largest is off by up to 2^-31 of that one, so a dim of out by
+ * up to 2^-31 times the sum of its |values| besides (larger weights: 2^-22 of
+ * themselves).
  *   q, group, out, lse, sm_scale : as quest_sparse_decode_attn
  *   mods      : NULL, or as above with one doc_starts entry per request
  *   workspace : device, >= quest_dense_decode_workspace_size(...) bytes, 16-B
@@ -642,8 +646,8 @@ QUEST_API quest_status quest_quant_read_kv(const quest_quant_cache* cache,
 
 /*
  * quest_quant_sparse_decode_attn — quest_sparse_decode_attn over a
- * quest_quant_cache: the same lists, results and errors, fp32 accuracy against
- * the stored numbers. Short lists go to a cluster each (one launch), the slots of
+ * quest_quant_cache: the same lists, results and errors, accurate against the
+ * stored numbers as quest_dense_decode_attn is with fp16. Short lists go to a cluster each (one launch), the slots of
  * many long ones are cut into equal runs, one per warp, as in
  * quest_dense_decode_attn; parts are joined by log-sum-exp, always in the same
  * order.

@@ -22,7 +22,9 @@
 //
 // fp16 on mma.sync m16n8k16, keys and dims as the 16 rows, the group's heads
 // as (up to) the 8 columns:  S^T = K Q^T,  O^T += V^T P^T.  P is passed as two
-// fp16 numbers, p = p1 + p2 to 2^-22, so the output keeps fp32 accuracy.
+// fp16 numbers, p = p1 + p2 to 2^-22 from 2^-9 of the largest weight on (which is 2^6
+// or more); below, p2 is subnormal and a weight is off by up to 2^-31 of the largest:
+// fp32 accuracy, unless values of such weights are far larger than the others.
 // fp32: plain FMA, a lane per (token, quarter of the dims) for the logits, a
 // lane per dims for the values.
 //

@@ -5,8 +5,8 @@
 // on mma.sync m16n8k16 in fp16: the codes of K as they are (exact), 2^e of a
 // token as a factor of its logit; the codes of V times 2^e (exact), since the
 // weights would leave fp16's range with it. The running softmax is
-// dense_decode.cuh's (WarpMma), so the output keeps fp32 accuracy against the
-// stored values.
+// dense_decode.cuh's (WarpMma): against the stored values, the output is as accurate
+// as it says there.
 //
 // Bound: HBM, 2 (D + 1) bytes a token and KV head, half of an fp16 cache; small
 // calls the chain launch - lengths - page ids - pages - join.
