@@ -584,7 +584,10 @@ QUEST_API quest_status quest_norm_rope_append_kv(const quest_cache* cache, const
  *                        [s][i][g][t][c][hi][lo] dim 32 i + 4 g + c of token
  *                        16 s + 8 hi + 2 t + lo
  *               K scales uint8 [S], V scales uint8 [S]: 127 + e (E8M0)
- *             (S = page_size)
+ *             (S = page_size). A pool filled by other means than the append holds to
+ *             this too: scales of 113 to 134 and no code of "not a number" (0x7f,
+ *             0xff) in a valid token. Nothing checks it; other bytes give wrong
+ *             numbers.
  *   summary : device, [n_phys, h_kv, 2, head_dim], fp16, or E4M3 codes with
  *             summary_fp8 = 1, as in quest_cache
  * Page scores: pass quest_score_pages(_per_head) a quest_cache of dtype

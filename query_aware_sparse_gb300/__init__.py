@@ -224,7 +224,8 @@ class QuantCache:
 
     pool: uint8 [n_phys, h_kv, quant_page_bytes(page_size, head_dim)] (the
     layout is quest_quant_cache's in quest.h; ``k_codes``, ``v_codes``,
-    ``k_scales`` and ``v_scales`` are views of its parts); summary:
+    ``k_scales`` and ``v_scales`` are views of its parts, and its only exponents
+    are -14 to 7); summary:
     [n_phys, h_kv, 2, head_dim], fp16 or, as torch.uint8, E4M3 codes. It goes
     to the quant_* calls and, for its summary, to the page scores; the calls
     that read fp16 or fp32 pages take the PagedCache of quant_read_kv.

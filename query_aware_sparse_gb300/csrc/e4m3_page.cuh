@@ -5,7 +5,7 @@
 //   K codes  [D / 64][S][64]                       dims of one token, 64 at a time
 //   V codes  [S / 16][D / 32][8][4][4][2][2]       [s][i][g][t][c][hi][lo] holds
 //            dim 32 i + 4 g + c of token 16 s + 8 hi + 2 t + lo
-//   K scales [S], V scales [S]                     exponent bytes (E8M0): 2^(b - 127)
+//   K scales [S], V scales [S]                     exponent bytes (E8M0): 2^(b - 127), 113 to 134
 // A code times its token's scale is the value; with exponents in [-14, 7] that is
 // always an fp16 number (E4M3 has 4 significant bits, its smallest step is 2^-9).
 #pragma once
