@@ -76,8 +76,8 @@ quest_status take_append(quest::NormAppendArgs& p, const quest_pages* pages, con
 }
 
 // Sizes that the decode kernels' grids and running sums take.
-bool decodable(const quest_pages* pages, int32_t h_kv, int32_t group) {
-  return pages->batch <= quest::kDecodeMaxBatch && (int64_t)pages->batch * h_kv * group <= INT32_MAX;
+bool decodable(int32_t batch, int32_t h_kv, int32_t group) {
+  return batch <= quest::kDecodeMaxBatch && (int64_t)batch * h_kv * group <= INT32_MAX;
 }
 
 quest_status quant_attn(const quest_quant_cache* cache, const quest_pages* pages, const void* q, int32_t group,
@@ -175,7 +175,7 @@ quest_status quest_quant_read_kv(const quest_quant_cache* cache, const quest_pag
 
 size_t quest_quant_decode_workspace_size(int32_t batch, int32_t h_kv, int32_t group, int32_t head_dim,
                                          int32_t page_size) {
-  if (batch <= 0 || batch > quest::kDecodeMaxBatch || h_kv <= 0 || !valid_group(group) ||
+  if (batch <= 0 || h_kv <= 0 || !valid_group(group) || !decodable(batch, h_kv, group) ||
       quest_quant_page_bytes(page_size, head_dim) == 0)
     return 0;
   return quest::quant_decode_workspace(batch, h_kv, group, head_dim);
@@ -191,7 +191,7 @@ quest_status quest_quant_sparse_decode_attn(const quest_quant_cache* cache, cons
   if ((st = check_pages(pages, true)) != QUEST_OK) return st;
   if (!valid_group(group) || k < 1) return QUEST_ERR_INVALID_ARG;
   if (pages->batch == 0) return QUEST_OK;
-  if (!decodable(pages, cache->h_kv, group)) return QUEST_ERR_UNSUPPORTED;
+  if (!decodable(pages->batch, cache->h_kv, group)) return QUEST_ERR_UNSUPPORTED;
   if (!sel_logical || !sel_phys) return QUEST_ERR_INVALID_ARG;
   return quant_attn(cache, pages, q, group, sel_logical, sel_phys, k, nullptr, out, lse, sm_scale, workspace,
                     workspace_bytes, stream);
@@ -207,7 +207,7 @@ quest_status quest_quant_dense_decode_attn(const quest_quant_cache* cache, const
   if (!valid_group(group)) return QUEST_ERR_UNSUPPORTED;
   if ((st = check_mods(mods)) != QUEST_OK) return st;
   if (pages->batch == 0) return QUEST_OK;
-  if (!decodable(pages, cache->h_kv, group)) return QUEST_ERR_UNSUPPORTED;
+  if (!decodable(pages->batch, cache->h_kv, group)) return QUEST_ERR_UNSUPPORTED;
   return quant_attn(cache, pages, q, group, nullptr, nullptr, 0, mods, out, lse, sm_scale, workspace,
                     workspace_bytes, stream);
 }
