@@ -59,7 +59,8 @@ __device__ __forceinline__ uint2 fetched8(uint32_t at) {
 }
 
 // Physical page of logical page lp of request r, or -1 (reported) where the
-// table or the pool has none. For the whole CTA.
+// table or the pool has none. For the whole CTA. (rope_append.cu has the same lines
+// in place: sharing them made that kernel slower.)
 __device__ __forceinline__ int page_of(const RopeAppendArgs& a, int r, int lp) {
   const int entry = a.page_indptr[r] + lp;
   if (lp >= a.page_indptr[r + 1] - a.page_indptr[r] || entry >= a.nnz) {

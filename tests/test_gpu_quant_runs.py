@@ -34,3 +34,17 @@ def test_more_units_than_the_device_holds(d, S, group):
     case = quant_case(440 + group, lens.tolist(), h_kv=8, group=group, d=d, S=S)
     for k in (9, border, border + 1):
         _sparse(case, k, seed=k, drop=0.1)
+
+
+@pytest.mark.parametrize("d,S,group", [(128, 16, 4), (64, 16, 8)])
+def test_clusters_look_up_their_tiles_more_than_once(d, S, group):
+    """Lists and a table of more tiles than the 32 that a warp of a cluster takes
+    from them at a time: 16 requests of 8 heads leave three CTAs per unit."""
+    rng = np.random.default_rng(group)
+    lens = rng.integers(0, 40, 16)
+    lens[2], lens[9] = 600 * S - 5, 0
+    case = quant_case(450 + group, lens.tolist(), h_kv=8, group=group, d=d, S=S)
+    assert 32 * 12 < case["table"].nnz <= 64 * 12
+    _dense(case)
+    _dense(case, ["cap", "window", "doc"], seed=6)
+    _sparse(case, 590, seed=2, drop=0.4)              # holes among the slots of a look
