@@ -448,6 +448,7 @@ class DecodeStep:
 
     def __init__(self, cache: PagedCache, table: PageTable, group: int, k: int, device=None,
                  n_sink: int = 0, n_local: int = 0):
+        cache.c                                                 # a QuantCache says here what it is not
         dev = device or cache.k_pool.device
         B, h = table.batch, cache.h_kv
         self.group, self.k = group, k
