@@ -48,3 +48,18 @@ def test_clusters_look_up_their_tiles_more_than_once(d, S, group):
     _dense(case)
     _dense(case, ["cap", "window", "doc"], seed=6)
     _sparse(case, 590, seed=2, drop=0.4)              # holes among the slots of a look
+
+
+@pytest.mark.parametrize("d,S,group", [(128, 16, 2), (64, 32, 8)])
+def test_a_batch_padded_with_empty_requests(d, S, group):
+    """A table of few pages for more units than the device holds at once: a CTA
+    each, most of them without a token."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rng = np.random.default_rng(group)
+    lens = np.zeros(4 * sms, int)
+    lens[rng.permutation(len(lens))[:30]] = rng.integers(1, S + 1, 30)
+    lens[-1] = 9 * S + 1
+    case = quant_case(460 + group, lens.tolist(), h_kv=1, group=group, d=d, S=S)
+    assert case["table"].nnz <= 4 * 12
+    _dense(case)
+    _dense(case, ["alibi", "prefix"], seed=7)
